@@ -83,7 +83,12 @@ typedef enum { KDA_W_BF16 = 0, KDA_W_FP8_E4M3 = 1 } kda_weight_dtype;
 #define KDA_DEVERR_TOKENS    0x10  /* kda_verify_resume: n_tokens[b] outside [1, T]; sequence skipped */
 #define KDA_DEVERR_SEQLEN    0x20  /* kda_prefill_varlen: cu_seqlens inconsistent for a sequence
                                       (negative, decreasing, past total_tokens or longer than
-                                      max_len); that sequence is skipped */
+                                      max_len); that sequence is skipped.  Paged cache: lengths,
+                                      token counts or offsets that do not fit the row */
+#define KDA_DEVERR_PAGE      0x40  /* paged cache: a page table entry outside [0, num_pages) where a
+                                      page is needed (its tokens are left out) */
+#define KDA_DEVERR_NOPAGES   0x80  /* kda_kv_extend: no free pages, or the row's table is full;
+                                      that sequence is left as it was */
 
 /* Weights of one KDA layer (read only). */
 typedef struct {
@@ -271,6 +276,144 @@ kda_status kda_prefill_noalloc(const kda_layer *layer, const kda_pool *pool, con
 /* Reads *pool->err_word into *host_err, then clears it (synchronises `stream`).  Returns
  * KDA_ERR_DEVICE when the word was nonzero, KDA_OK otherwise. */
 kda_status kda_get_error(const kda_pool *pool, int32_t *host_err, void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Paged key-value cache and the attention layers that read it: the softmax-attention layers
+ * that stand between KDA layers in a hybrid model, in the same forms (decode, draft verify,
+ * packed prefill).  No page describes them; the formulas are the usual ones and stated here.
+ *
+ * A cache holds the keys and values of `num_layers` attention layers in pages of page_size
+ * tokens.  Row r of the page table is a sequence of seq_lens[r] tokens: token j lives in page
+ * page_table[r][j / page_size] at j % page_size, and entries past the last page are -1.
+ * page_refs[p] counts the table entries that name page p; a page with 0 is free.  One step of
+ * a serving loop is kda_kv_extend once (pages and lengths, all layers together), then for each
+ * layer kda_kv_append (its new keys and values) and kda_attn_decode or kda_attn_prefill.  The
+ * lengths that append and attention read are those after extend: the n new tokens of a row of
+ * length L are its positions L - n .. L - 1.  Drafts that were not accepted are given back by
+ * kda_kv_truncate.
+ *
+ * The rules of the other entries hold: nothing is allocated, synchronised or read on the host,
+ * every call can be captured, host-visible errors return before a launch, device-side ones set
+ * bits in *err_word and leave the sequence out.  All kernels are launched with programmatic
+ * dependent launch and read nothing before their dependency wait. */
+
+/* Element types of queries, outputs and caches. */
+typedef enum { KDA_T_BF16 = 0, KDA_T_F16 = 1, KDA_T_E4M3 = 2 } kda_elem_type;
+
+typedef struct {
+    void *k, *v;             /* [num_layers, num_pages, num_kv_heads, page_size, head_dim], 16-byte
+                                aligned; kv_dtype */
+    int32_t kv_dtype;        /* kda_elem_type */
+    int32_t num_layers, num_pages, num_kv_heads;
+    int32_t page_size;       /* 16, 32, 64 or 128 */
+    int32_t head_dim;        /* 64 or 128 */
+    int32_t rows, max_pages; /* page table: rows x max_pages */
+    int32_t *page_table;     /* [rows, max_pages] */
+    int32_t *seq_lens;       /* [rows] */
+    int32_t *page_refs;      /* [num_pages] */
+    const float *k_scale;    /* [num_layers, num_kv_heads], needed with KDA_T_E4M3 (else ignored): */
+    const float *v_scale;    /*   a stored code c stands for scale * c */
+    int32_t *err_word;       /* device int32, zero-initialised by the caller */
+} kda_kv_cache;
+
+/* Device scratch of the page calls below, owned by the caller, 256-byte aligned, no
+ * initialisation needed.  Calls that may overlap on the GPU need scratch of their own. */
+size_t kda_kv_workspace_size(const kda_kv_cache *cache);
+
+/* Makes room for n_tokens[i] more tokens in row rows[i] (n_all where n_tokens is NULL) and adds
+ * them to its length.  New pages are the lowest free page ids, given out in the order of i and
+ * then of the row's pages.  Where the row's last page is partly filled and other rows use it
+ * too, the row gets a copy of it first (the copied page's id comes before those of the added
+ * pages), in every layer.  A row for which not enough free pages are left (after those asked
+ * for by all earlier rows of the call) or whose table is full sets KDA_DEVERR_NOPAGES and is
+ * left as it was.  rows[i] must be distinct: a repeated row sets KDA_DEVERR_SLOT and only its
+ * first entry counts; so does a row outside [0, cache->rows).  A negative count sets
+ * KDA_DEVERR_TOKENS.  0 tokens leave a row as it is. */
+kda_status kda_kv_extend(const kda_kv_cache *cache, const int32_t *rows, const int32_t *n_tokens,
+                         int32_t n_all, int32_t B, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* Cuts row rows[i] to new_lens[i] tokens (0 frees it): pages past the new length are given back,
+ * free once no other row uses them.  A length above the present one or negative sets
+ * KDA_DEVERR_SEQLEN and the row is left as it was.  rows distinct as above. */
+kda_status kda_kv_truncate(const kda_kv_cache *cache, const int32_t *rows, const int32_t *new_lens,
+                           int32_t B, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Row dst_rows[i] gives its pages back and becomes a copy of row src_rows[i] that shares all of
+ * its pages; no data moves until one of them extends past a shared, partly filled page.
+ * A destination that is repeated, out of range or also a source of the call sets
+ * KDA_DEVERR_SLOT and its entry is left out (a repeated one counts once). */
+kda_status kda_kv_fork(const kda_kv_cache *cache, const int32_t *src_rows, const int32_t *dst_rows,
+                       int32_t n, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Moves the pages in use to the ids [0, pages in use): with n pages in use, the ones with ids
+ * >= n go, in ascending order, to the free ids below n in ascending order, in every layer.
+ * The whole page table, the counts and the data follow.
+ *   remap  int32 [num_pages] (device): receives each used page's new id, -1 for free pages */
+kda_status kda_kv_compact(const kda_kv_cache *cache, int32_t *remap, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Writes new keys and values of one layer into their pages (rounded to nearest even to E4M3 after
+ * division by the layer's scale, clamped to +-448, where the cache holds codes; NaN stays NaN).
+ * Either cu_seqlens is NULL and k, v hold B sequences of T tokens, of which the first
+ * n_tokens[b] count (all T where n_tokens is NULL), seq_stride apart; or cu_seqlens [B+1] gives
+ * sequence b the rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of T = total packed tokens.
+ * A sequence with more new tokens than its row's length sets KDA_DEVERR_SEQLEN and is skipped.
+ *   k, v      KDA_T_BF16 or KDA_T_F16 (the cache's own type, or either with an E4M3 cache), head
+ *             h of token t at seq * seq_stride + t * token_stride + h * head_stride (elements;
+ *             multiples of 8, pointers 16-byte aligned), head_dim elements contiguous */
+typedef struct {
+    int32_t dtype;           /* kda_elem_type: KDA_T_BF16 or KDA_T_F16 */
+    int64_t seq_stride;      /* ignored with cu_seqlens */
+    int64_t token_stride;
+    int64_t head_stride;
+} kda_tokens_layout;
+kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t *rows, int32_t B,
+                         int32_t T, const int32_t *n_tokens, const int32_t *cu_seqlens,
+                         const void *k, const kda_tokens_layout *k_layout, const void *v,
+                         const kda_tokens_layout *v_layout, void *stream);
+
+/* Attention of new tokens over a layer's pages.  A token at position p sees key j where j <= p and
+ * (window == 0, or j > p - window, or j < sinks): a causal layer, or one with a sliding window
+ * of `window` keys (the token's own among them) and `sinks` first tokens that stay visible.
+ *   s_j = scale * q . k_j;  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m);
+ *   lse = m + log(sum_j exp(s_j - m)).  A token that sees no key (a row shorter than the call's
+ *   tokens puts its first ones at negative positions) gets out = 0, lse = -inf.
+ * Query head h reads kv head h / (num_q_heads / num_kv_heads).  Keys that no token of the call
+ * sees are not read (their table entries may be -1, their contents anything).  Products are
+ * taken in the query's type (a 16-bit cache must have it too; E4M3 codes are exact in both) with
+ * FP32 sums; the softmax statistics are FP32.
+ * Workspace: kda_attn_workspace_size() bytes, 256-byte aligned, ZEROED by the caller once; every
+ * call leaves it ready for the next.  Calls that may overlap on the GPU need one each. */
+typedef struct {
+    int32_t num_q_heads;     /* a multiple of num_kv_heads, at most 64 per kv head */
+    float scale;             /* finite, >= 0; usually 1 / sqrt(head_dim) */
+    int32_t window;          /* 0 = none */
+    int32_t sinks;           /* >= 0; used with a window */
+    kda_tokens_layout q;     /* layout of the queries, as in kda_kv_append */
+} kda_attn_desc;
+size_t kda_attn_workspace_size(const kda_kv_cache *cache);
+
+/* Decode and draft verify: T (1..16) new tokens for each of B rows, of which n_tokens[b] in
+ * [0, T] count (all T where n_tokens is NULL).  out [B, T, num_q_heads, head_dim] in the
+ * query's type, lse fp32 [B, T, num_q_heads] or NULL; entries t >= n_tokens[b] are not written.
+ * The cache's length is split over the GPU and joined inside the call, in a fixed order. */
+kda_status kda_attn_decode(const kda_kv_cache *cache, int32_t layer, const kda_attn_desc *desc,
+                           const int32_t *rows, int32_t B, int32_t T, const int32_t *n_tokens,
+                           const void *q, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Packed prefill: sequence b's new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of q, out
+ * [total_tokens, num_q_heads, head_dim] and lse [total_tokens, num_q_heads] (or NULL); max_len
+ * bounds every sequence's count (host; no device read).  A sequence whose offsets are out of
+ * order or range, or longer than max_len, sets KDA_DEVERR_SEQLEN and is skipped. */
+kda_status kda_attn_prefill(const kda_kv_cache *cache, int32_t layer, const kda_attn_desc *desc,
+                            const int32_t *rows, int32_t B, const int32_t *cu_seqlens,
+                            int32_t total_tokens, int32_t max_len, const void *q, void *out,
+                            float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* kda_get_error for a cache: reads *cache->err_word into *host_err, then clears it. */
+kda_status kda_kv_get_error(const kda_kv_cache *cache, int32_t *host_err, void *stream);
 
 /* Static string for a status code. */
 const char *kda_status_string(kda_status s);

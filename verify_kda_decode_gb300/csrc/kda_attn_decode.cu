@@ -1,0 +1,516 @@
+// kda_attn_decode.cu -- attention of a few new tokens per sequence over a paged key-value cache
+// (kda_attn_decode): decode, draft verify and mixed steps.
+//
+// Mathematics.  For one sequence and key head the rows are the call's (token, query head) pairs,
+// R = n * G of them; per block of keys S^T = K Q^T, P = exp2(S^T - m) with a running maximum m and
+// sum l per row, O^T += V^T P^T, both products on mma.sync m16n8k16 with keys (or head dims) as the
+// 16 rows and 8 query rows as columns.  Keys and head dims are summed over, so their order within a
+// block is free: each thread takes 16 contiguous bytes of a key as its A fragments for two k-steps
+// and takes the same elements of q, and V's fragments pair the same element of two keys (one byte
+// permutation a word).  P^T becomes the B operand by transposing 8x8 matrices between lanes.
+//
+// Bound.  Every key and value byte is used for R rows only: HBM bound (R <= 32 needs at most 1/8 of
+// the tensor rate).  So the design is about bytes in flight and an even split.  Each warp owns a ring
+// of cp.async stages (16 keys and values a stage; 24 KiB a warp, 192 KiB an SM with eight warps,
+// against about 45 KiB that the latency-bandwidth product asks of an SM), with no CTA barrier inside
+// a run of keys.  All tiles of all (sequence, key head, row block) units are laid out in one line and
+// cut into equal runs, one per CTA, so ragged lengths load the SMs evenly; a unit that spans several
+// CTAs leaves partial (m, l, O) in the workspace and the CTA that finishes last joins them in the
+// fixed order of the pieces.  No result depends on which CTA that is.
+//
+// Rows of a page that no token sees are not read: cp.async writes zeros for them, so whatever the
+// page holds there (NaN included) cannot reach the products.
+#include "kda_attn_common.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kStep = 16;                 // keys of one warp step
+constexpr int kTileKeys = kWarps * kStep; // keys of one tile: 16 for each warp
+constexpr int kMaxCtas = 1024;            // bound of the grid, sizes the workspace
+constexpr int kMaxRows = 32;
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    if constexpr (T::is_half)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8x8 matrix of 16-bit elements held one row per quad.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int ES = FP8 ? 1 : 2;
+    static constexpr int RB = D * ES;                     // bytes of a key
+    static constexpr int CH = RB / 16;                    // its 16-byte chunks
+    static constexpr int STAGE = 2 * kStep * RB;          // keys, then values
+    static constexpr int NS = 24576 / STAGE > 8 ? 8 : 24576 / STAGE;
+    static constexpr int RING = kWarps * NS * STAGE;
+    // the pieces of a unit are merged in the ring's place
+    static constexpr int merge_bytes(int nb) { return kWarps * 8 * nb * (D + 2) * 4; }
+    static constexpr int smem(int nb) { return RING > merge_bytes(nb) ? RING : merge_bytes(nb); }
+    // chunk c of row r is stored at chunk c ^ swz(r): conflict-free for the fragment loads
+    // (K: eight lanes read four chunks of two rows; V: two chunks of four even rows)
+    static __device__ __forceinline__ int swz_k(int r) { return CH >= 8 ? 4 * (r & 1) : 0; }
+    static __device__ __forceinline__ int swz_v(int r) { return CH >= 8 ? 2 * ((r >> 1) & 3) : (r >> 1) & 3; }
+    // head dim of the first of the two elements that accumulator block m of lane group g holds
+    static __device__ __forceinline__ int dim(int m, int g) { return FP8 ? (D / 8) * g + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3); }
+};
+
+struct Partials {   // workspace: counters, then for each CTA two slots of (m, l, O)
+    int *count;
+    float *data;
+    static constexpr size_t slot_floats(int D) { return (size_t)kMaxRows * (D + 2); }
+    __device__ float *slot(int s, int D) const { return data + (size_t)s * slot_floats(D); }
+};
+
+template <int D, typename Q, bool FP8, int NB>
+__global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const AttnParams p)
+{
+    using C = Cfg<D, FP8>;
+    using P = std::conditional_t<FP8, Half, Q>;   // type of the second product
+    constexpr int MT = D / 16;                    // accumulator blocks (16 head dims)
+    constexpr int ROWS = 8 * NB;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long sh_prefix, sh_warp[kWarps];
+    __shared__ int sh_b, sh_last;
+    const PagedCache &c = p.c;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, cc = lane & 3;
+    const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
+    Partials part;
+    part.count = reinterpret_cast<int *>(p.ws);
+    part.data = reinterpret_cast<float *>(p.ws + kMaxCtas * sizeof(int));
+
+    grid_dependency_wait();
+
+    // ---- this CTA's run of tiles
+    auto load_seq = [&](int b, bool report) { return seq_info(c, p.rows[b], p.n_tokens ? p.n_tokens[b] : p.T, p.T, report); };
+    auto tiles_of = [&](const SeqInfo &s, int &kt, int &mt) -> long long {   // kt tiles in each of Hkv * mt units
+        kt = mt = 0;
+        if (!s.ok || s.n == 0) return 0;
+        const KeyRange<kTileKeys> r(s.len - s.n, s.len - 1, s.len, W, S);
+        kt = max(1, r.count);
+        mt = (s.n * p.G + ROWS - 1) / ROWS;
+        return (long long)kt * mt * c.Hkv;
+    };
+    const int per = (p.B + kThreads - 1) / kThreads, b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+    long long mine = 0;
+    int kt, mt;
+    for (int b = b_lo; b < b_hi; b++) mine += tiles_of(load_seq(b, blockIdx.x == 0), kt, mt);
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) sh_warp[w] = before;
+    __syncthreads();
+    before -= mine;
+    long long total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; i++) {
+        if (i < w) before += sh_warp[i];
+        total += sh_warp[i];
+    }
+    const long long chunk = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+    const long long begin = blockIdx.x * chunk, end = min(total, begin + chunk);
+    if (begin >= end) return;
+    if (begin >= before && begin < before + mine) {
+        long long at = before;
+        for (int b = b_lo; b < b_hi; b++) {
+            const long long n = tiles_of(load_seq(b, false), kt, mt);
+            if (begin < at + n) {
+                sh_b = b;
+                sh_prefix = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    int b = sh_b;
+    long long prefix = sh_prefix;
+    SeqInfo seq = load_seq(b, false);
+    long long seq_tiles = tiles_of(seq, kt, mt);
+
+    const uint32_t ring = smem_u32(smem) + w * (C::NS * C::STAGE);
+    uint8_t *ring_p = smem + w * (C::NS * C::STAGE);
+    float *mg = reinterpret_cast<float *>(smem);          // merge buffer: O [warp][ROWS][D], m, l [warp][ROWS]
+    float *mg_m = mg + kWarps * ROWS * D, *mg_l = mg_m + kWarps * ROWS;
+
+    long long at = begin;
+    while (at < end) {
+        while (at >= prefix + seq_tiles) {   // next sequence with work (there is one: at < total)
+            prefix += seq_tiles;
+            seq = load_seq(++b, false);
+            seq_tiles = tiles_of(seq, kt, mt);
+        }
+        const int local = (int)((at - prefix) / kt);
+        const int h = local / mt, mb = local % mt;
+        const long long u0 = prefix + (long long)local * kt;              // the unit's tiles [u0, u0 + kt)
+        const int ta = (int)(at - u0), tb = (int)min((long long)kt, end - u0);
+        const int n_rows = min(ROWS, seq.n * p.G - mb * ROWS);
+        const int p0 = seq.len - seq.n;
+        const KeyRange<kTileKeys> kr(p0, seq.len - 1, seq.len, W, S);
+        const int lo_all = (int)max(0ll, (long long)seq.len - W);         // every token sees [lo_all, p0]
+        const size_t head_bytes = (size_t)c.ps * C::RB;
+        const size_t layer_off = (size_t)p.layer * c.pages;
+
+        // queries: rows nb * 8 + g, the elements this thread multiplies
+        uint32_t qf[NB][D / 16][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            const int r = nb * 8 + g;
+            const int t = (mb * ROWS + r) / p.G, hq = h * p.G + (mb * ROWS + r) % p.G;
+            const uint16_t *src = p.q + b * p.ql.seq + t * p.ql.token + hq * p.ql.head;
+#pragma unroll
+            for (int j = 0; j < D / 32; j++) {
+                // 16-bit cache: chunk cc + 4 j of 8 elements; E4M3: 16-element chunks, this is half (j & 1) of chunk cc + 4 (j / 2)
+                const int e = FP8 ? 16 * (cc + 4 * (j >> 1)) + 8 * (j & 1) : 8 * (cc + 4 * j);
+                const uint4 x = r < n_rows ? __ldg(reinterpret_cast<const uint4 *>(src + e)) : make_uint4(0, 0, 0, 0);
+                qf[nb][2 * j][0] = x.x;
+                qf[nb][2 * j][1] = x.y;
+                qf[nb][2 * j + 1][0] = x.z;
+                qf[nb][2 * j + 1][1] = x.w;
+            }
+        }
+        const float sc = p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
+
+        float acc[MT][NB][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[m][nb][i] = 0.f;
+        float row_m[NB][2], row_l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) row_m[nb][0] = row_m[nb][1] = -INFINITY, row_l[nb][0] = row_l[nb][1] = 0.f;
+
+        // page ids of this warp's next 32 steps, one per lane, and of the 32 after them
+        auto key_of = [&](int t) { return kr.tile(t) * kTileKeys + w * kStep; };
+        auto step_used = [&](int k0) { return k0 < kr.end && (k0 + kStep > kr.lo || k0 < S); };
+        auto load_pages = [&](int t0) {
+            const int t = t0 + lane;
+            if (t >= tb) return -1;
+            const int k0 = key_of(t);
+            return step_used(k0) ? __ldg(c.table + (size_t)seq.row * c.width + (k0 >> c.ps_log2)) : -1;
+        };
+        int pages_at = ta, pages_now = load_pages(ta), pages_next = load_pages(ta + 32);
+
+        uint32_t bad = 0;   // bit s: the step in stage s has no page
+        auto issue = [&](int t, int stage) {
+            if (t < tb) {
+                if (t - pages_at >= 32) {
+                    pages_at += 32;
+                    pages_now = pages_next;
+                    pages_next = load_pages(pages_at + 32);
+                }
+                const int k0 = key_of(t);
+                const int page = __shfl_sync(~0u, pages_now, t - pages_at);
+                if (step_used(k0)) {
+                    const bool ok = (unsigned)page < (unsigned)c.pages;
+                    bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
+                    if (!ok) {
+                        if (lane == 0) atomicOr(c.err, KDA_DEVERR_PAGE);
+                    } else {
+                        const size_t off = ((layer_off + page) * c.Hkv + h) * head_bytes + (size_t)(k0 & (c.ps - 1)) * C::RB;
+                        uint8_t *dk = ring_p + stage * C::STAGE, *dv = dk + kStep * C::RB;
+#pragma unroll
+                        for (int i = 0; i < kStep * C::CH / 32; i++) {
+                            const int q = i * 32 + lane, r = q / C::CH, x = q % C::CH, j = k0 + r;
+                            const uint32_t n = j < kr.end && (j >= kr.lo || j < S) ? 16 : 0;
+                            cp_async16(dk + r * C::RB + ((x ^ C::swz_k(r)) * 16), c.k + off + (size_t)q * 16, n);
+                            cp_async16(dv + r * C::RB + ((x ^ C::swz_v(r)) * 16), c.v + off + (size_t)q * 16, n);
+                        }
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+
+        int st_in = 0, st_out = 0;
+#pragma unroll
+        for (int i = 0; i < C::NS - 1; i++) issue(ta + i, st_in++);
+        for (int t = ta; t < tb; t++) {
+            issue(t + C::NS - 1, st_in);
+            st_in = st_in + 1 == C::NS ? 0 : st_in + 1;
+            cp_async_wait<C::NS - 1>();
+            __syncwarp();
+            const int k0 = key_of(t), stage = st_out;
+            st_out = st_out + 1 == C::NS ? 0 : st_out + 1;
+            if (step_used(k0) && !(bad >> stage & 1)) {
+                const uint32_t kb = ring + stage * C::STAGE, vb = kb + kStep * C::RB;
+                float s[NB][4];
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < C::CH / 4; j++) {
+                    const uint4 x = lds128(kb + g * C::RB + (((cc + 4 * j) ^ C::swz_k(g)) * 16));
+                    const uint4 y = lds128(kb + (g + 8) * C::RB + (((cc + 4 * j) ^ C::swz_k(g + 8)) * 16));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            const uint32_t a[4] = {e4m3x2_as<Q>(xs[u], 0), e4m3x2_as<Q>(ys[u], 0), e4m3x2_as<Q>(xs[u], 1), e4m3x2_as<Q>(ys[u], 1)};
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++) mma16816<Q>(s[nb], a, qf[nb][4 * j + u][0], qf[nb][4 * j + u][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 2; u++) {
+                            const uint32_t a[4] = {xs[2 * u], ys[2 * u], xs[2 * u + 1], ys[2 * u + 1]};
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++) mma16816<Q>(s[nb], a, qf[nb][2 * j + u][0], qf[nb][2 * j + u][1]);
+                        }
+                    }
+                }
+                // s[nb]: keys k0 + g (+ 8), rows nb * 8 + 2 cc (+ 1); in units of log2
+                const bool all = k0 + kStep - 1 <= p0 && (k0 >= lo_all || k0 + kStep <= S);
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        s[nb][i] *= sc;
+                        if (!all) {
+                            const int tok = (mb * ROWS + nb * 8 + 2 * cc + (i & 1)) / p.G;
+                            if (!key_visible(k0 + g + 8 * (i >> 1), p0 + tok, W, S)) s[nb][i] = -INFINITY;
+                        }
+                    }
+                uint32_t pf[NB][2];
+                bool grown = false;
+                float alpha[NB][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        float mx = fmaxf(s[nb][i], s[nb][i + 2]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                        const float m_new = fmaxf(row_m[nb][i], mx);
+                        const float base = m_new == -INFINITY ? 0.f : m_new;   // a row that has seen no key yet
+                        grown |= m_new > row_m[nb][i];
+                        alpha[nb][i] = exp2f(row_m[nb][i] - base);
+                        row_m[nb][i] = m_new;
+                        s[nb][i] = exp2f(s[nb][i] - base);
+                        s[nb][i + 2] = exp2f(s[nb][i + 2] - base);
+                        row_l[nb][i] = row_l[nb][i] * alpha[nb][i] + (s[nb][i] + s[nb][i + 2]);
+                    }
+                    // P is rounded to the product's 16-bit type (relative error 2^-9 or 2^-12, as the
+                    // output's own rounding); l sums it unrounded
+                    pf[nb][0] = transpose8x8(P::pack(s[nb][0], s[nb][1]));
+                    pf[nb][1] = transpose8x8(P::pack(s[nb][2], s[nb][3]));
+                }
+                if (__any_sync(~0u, grown)) {
+#pragma unroll
+                    for (int m = 0; m < MT; m++)
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int i = 0; i < 4; i++) acc[m][nb][i] *= alpha[nb][i & 1];
+                }
+                const int kk[4] = {2 * cc, 2 * cc + 1, 2 * cc + 8, 2 * cc + 9};
+                auto pv = [&](int m, const uint32_t v0, const uint32_t v1, const uint32_t v2, const uint32_t v3) {
+                    const uint32_t a[4] = {__byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632),
+                                           __byte_perm(v2, v3, 0x5410), __byte_perm(v2, v3, 0x7632)};
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++) mma16816<P>(acc[m][nb], a, pf[nb][0], pf[nb][1]);
+                };
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int hh = 0; hh < D / 64; hh++) {
+                        uint32_t v[4][4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const uint4 x = lds128(vb + kk[i] * C::RB + (((8 * hh + g) ^ C::swz_v(kk[i])) * 16));
+                            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; i++) pv(4 * hh + i, v[0][i], v[1][i], v[2][i], v[3][i]);
+                    }
+                } else {
+                    constexpr int NW = D / 32;   // words of 4 codes per thread and key
+                    uint32_t v[4][NW];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if constexpr (NW == 4) {
+                            const uint4 x = lds128(vb + kk[i] * C::RB + ((g ^ C::swz_v(kk[i])) * 16));
+                            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                        } else {
+                            const uint2 x = lds64(vb + kk[i] * C::RB + (((g >> 1) ^ C::swz_v(kk[i])) * 16) + 8 * (g & 1));
+                            v[i][0] = x.x, v[i][1] = x.y;
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < NW; u++)
+#pragma unroll
+                        for (int hf = 0; hf < 2; hf++)
+                            pv(2 * u + hf, e4m3x2_half2(v[0][u], hf), e4m3x2_half2(v[1][u], hf), e4m3x2_half2(v[2][u], hf), e4m3x2_half2(v[3][u], hf));
+                }
+            }
+            __syncwarp();   // the stage is read: the next issue may overwrite it
+        }
+        cp_async_wait<0>();
+
+        // ---- the four warps' (m, l, O) into one
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) row_l[nb][i] += __shfl_xor_sync(~0u, row_l[nb][i], o);
+        __syncthreads();   // every warp is done with its ring
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int r = nb * 8 + 2 * cc + i;
+                if (g == 0) {
+                    mg_m[w * ROWS + r] = row_m[nb][i];
+                    mg_l[w * ROWS + r] = row_l[nb][i];
+                }
+                if (r < n_rows) {
+#pragma unroll
+                    for (int m = 0; m < MT; m++)
+                        *reinterpret_cast<float2 *>(&mg[(w * ROWS + r) * D + C::dim(m, g)]) = make_float2(acc[m][nb][i], acc[m][nb][2 + i]);
+                }
+            }
+        __syncthreads();
+
+        const int f = (int)(u0 / chunk), l = (int)((u0 + kt - 1) / chunk);   // CTAs that hold the unit's pieces
+        const float v_scale = FP8 ? c.v_scale[p.layer * c.Hkv + h] : 1.f;
+        auto store = [&](int r, int d, float4 o, float l_sum, float m) {   // 4 outputs of a row
+            const int t = (mb * ROWS + r) / p.G, hq = h * p.G + (mb * ROWS + r) % p.G;
+            const size_t row = ((size_t)b * p.T + t) * p.Hq + hq;
+            const float inv = l_sum == 0.f ? 0.f : v_scale / l_sum;
+            // a row that saw no key holds only zeros: 0 * 0
+            *reinterpret_cast<uint2 *>(p.out + row * D + d) = make_uint2(Q::pack(o.x * inv, o.y * inv), Q::pack(o.z * inv, o.w * inv));
+            if (p.lse && d == 0) p.lse[row] = l_sum == 0.f ? -INFINITY : (m + log2f(l_sum)) * kLn2;
+        };
+        float *slot = part.slot((int)blockIdx.x * 2 + (f == (int)blockIdx.x), D);
+        for (int x = tid; x < n_rows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), d = x % (D / 4) * 4;
+            float m = -INFINITY, ls = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; i++) m = fmaxf(m, mg_m[i * ROWS + r]);
+            const float base = m == -INFINITY ? 0.f : m;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kWarps; i++) {
+                const float a = exp2f(mg_m[i * ROWS + r] - base);
+                const float4 y = *reinterpret_cast<const float4 *>(&mg[(i * ROWS + r) * D + d]);
+                ls += a * mg_l[i * ROWS + r];
+                o.x += a * y.x, o.y += a * y.y, o.z += a * y.z, o.w += a * y.w;
+            }
+            if (f == l) store(r, d, o, ls, m);
+            else {
+                __stcg(reinterpret_cast<float4 *>(slot + 2 * kMaxRows + r * D + d), o);
+                if (d == 0) {
+                    __stcg(slot + r, m);
+                    __stcg(slot + kMaxRows + r, ls);
+                }
+            }
+        }
+        if (f != l) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int done = atomicAdd(&part.count[f], 1);
+                sh_last = done == l - f;
+                if (done == l - f) part.count[f] = 0;   // ready for the next call
+                __threadfence();
+            }
+            __syncthreads();
+            if (sh_last) {
+                const int n = l - f + 1;
+                for (int x = tid; x < n_rows * (D / 4); x += kThreads) {
+                    const int r = x / (D / 4), d = x % (D / 4) * 4;
+                    float m = -INFINITY, ls = 0.f;
+#pragma unroll 8
+                    for (int i = 0; i < n; i++) m = fmaxf(m, __ldcg(part.slot(2 * (f + i) + (i == 0), D) + r));
+                    const float base = m == -INFINITY ? 0.f : m;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int i = 0; i < n; i++) {
+                        const float *q = part.slot(2 * (f + i) + (i == 0), D);
+                        const float a = exp2f(__ldcg(q + r) - base);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(q + 2 * kMaxRows + r * D + d));
+                        ls += a * __ldcg(q + kMaxRows + r);
+                        o.x += a * y.x, o.y += a * y.y, o.z += a * y.z, o.w += a * y.w;
+                    }
+                    store(r, d, o, ls, m);
+                }
+            }
+        }
+        __syncthreads();   // the merge buffer is read: the next run's copies may land in it
+        at = u0 + tb;
+    }
+}
+
+template <int D, typename Q, bool FP8, int NB>
+cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
+{
+    static KernelSetup setup;
+    constexpr int smem = Cfg<D, FP8>::smem(NB);
+    int resident = 0;
+    const cudaError_t e = setup.get(kda_attn_decode_kernel<D, Q, FP8, NB>, kThreads, smem, 0, &resident);
+    if (e != cudaSuccess) return e;
+    if (resident < 1) return cudaErrorLaunchOutOfResources;
+    return launch_pdl(kda_attn_decode_kernel<D, Q, FP8, NB>, dim3((unsigned)min(resident, kMaxCtas)), dim3(kThreads), smem, stream, p);
+}
+
+// Row blocks of 8, 16 or 32: the smallest that holds the rows of a sequence and key head, at most 32
+// (more rows read the keys again from L2).
+template <int D, typename Q, bool FP8>
+cudaError_t launch_rows(const AttnParams &p, cudaStream_t stream)
+{
+    const int rows = p.T * p.G;
+    if (rows <= 8) return launch_as<D, Q, FP8, 1>(p, stream);
+    if (rows <= 16) return launch_as<D, Q, FP8, 2>(p, stream);
+    return launch_as<D, Q, FP8, 4>(p, stream);
+}
+
+template <int D>
+cudaError_t launch_types(const AttnParams &p, cudaStream_t stream)
+{
+    if (p.c.dtype == KDA_T_E4M3) return p.f16 ? launch_rows<D, Half, true>(p, stream) : launch_rows<D, Bf16, true>(p, stream);
+    return p.f16 ? launch_rows<D, Half, false>(p, stream) : launch_rows<D, Bf16, false>(p, stream);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace(int D) { return kMaxCtas * sizeof(int) + 2 * kMaxCtas * Partials::slot_floats(D) * sizeof(float); }
+
+cudaError_t launch_attn_decode(const AttnParams &p, cudaStream_t stream)
+{
+    return p.c.D == 128 ? launch_types<128>(p, stream) : launch_types<64>(p, stream);
+}
+
+}  // namespace kda
