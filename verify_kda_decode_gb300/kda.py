@@ -129,10 +129,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device: torch.device) -> int:
     """The cudaStream_t to launch on: the given stream (a torch.cuda.Stream or a raw handle), or
     the current stream of the tensors' device."""
     if stream is None:
+        if _raw_stream is not None:   # the same handle without building a Stream object
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

@@ -87,13 +87,25 @@ class KdaKvCache:
     def num_pages(self) -> int:
         return self.k.shape[1]
 
+    def __setattr__(self, name, value):
+        # another tensor in a field: the struct, the workspaces and what was checked against it go
+        d = self.__dict__
+        d[name] = value
+        if not name.startswith("_"):
+            for k in ("_c_struct", "_kv_ws", "_attn_ws", "_plans"):
+                d.pop(k, None)
+
     def c_struct(self) -> _Cache:
-        # checked and built once while the same tensors are attached
-        ts = (self.k, self.v, self.page_table, self.seq_lens, self.page_refs, self.k_scale, self.v_scale, self.err_word)
-        key = tuple((id(t), t.data_ptr(), t.shape, t.dtype) if t is not None else None for t in ts)
-        cached = self.__dict__.get("_c_struct")
-        if cached is not None and cached[0] == key:
-            return cached[1]
+        return self._struct()[0]
+
+    def _struct(self):
+        """(struct, reference to it), checked and built once while the same storages are attached."""
+        d = self.__dict__
+        ptrs = (self.k.data_ptr(), self.v.data_ptr(), self.page_table.data_ptr(), self.seq_lens.data_ptr(),
+                self.page_refs.data_ptr(), self.err_word.data_ptr())
+        cached = d.get("_c_struct")
+        if cached is not None and cached[2] == ptrs:
+            return cached
         if self.k.dtype not in _TYPES:
             raise TypeError(f"k: dtype {self.k.dtype}, expected bfloat16, float16 or float8_e4m3fn")
         if self.k.dim() != 5:
@@ -118,21 +130,24 @@ class KdaKvCache:
         st = _Cache(_ptr(self.k), _ptr(self.v), _TYPES[self.k.dtype], layers, pages, Hkv, ps, D, rows, width,
                     _ptr(self.page_table), _ptr(self.seq_lens), _ptr(self.page_refs),
                     _ptr(self.k_scale) if fp8 else None, _ptr(self.v_scale) if fp8 else None, _ptr(self.err_word))
-        self.__dict__["_c_struct"] = (key, st)
-        return st
+        for k in ("_kv_ws", "_attn_ws", "_plans"):
+            d.pop(k, None)
+        d["_c_struct"] = cached = (st, ctypes.byref(st), ptrs, dev)
+        return cached
 
     def _workspace(self, kind: str, given: Optional[torch.Tensor]) -> Tuple[int, int]:
         """(pointer, bytes) of the given workspace, or of the cache's own (zeroed when made)."""
         if given is not None:
+            if given.device != self.device or not given.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on the cache's device")
             return given.data_ptr(), given.numel() * given.element_size()
-        st = self.__dict__["_c_struct"][1]
-        own = self.__dict__.get("_" + kind)
-        if own is None or own[0] is not st:
-            size = _lib.kda_kv_workspace_size if kind == "kv_ws" else _lib.kda_attn_workspace_size
-            t = torch.zeros(max(256, int(size(ctypes.byref(st)))), dtype=torch.uint8, device=self.device)
-            own = (st, t, t.data_ptr(), t.numel())
-            self.__dict__["_" + kind] = own
-        return own[2], own[3]
+        own = self.__dict__.get(kind)
+        if own is None:
+            size = _lib.kda_kv_workspace_size if kind == "_kv_ws" else _lib.kda_attn_workspace_size
+            t = torch.zeros(max(256, int(size(self._struct()[1]))), dtype=torch.uint8, device=self.device)
+            own = (t.data_ptr(), t.numel(), t)
+            self.__dict__[kind] = own
+        return own[0], own[1]
 
 
 def kda_kv_workspace_size(cache: KdaKvCache) -> int:
@@ -148,55 +163,59 @@ def _ints(t: torch.Tensor, name: str, n: int, dev) -> int:
     return t.data_ptr()
 
 
-def _batch(rows: torch.Tensor) -> int:
-    if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
-        raise ValueError("rows must be an int32 tensor [B]")
-    return rows.shape[0]
+def _rows(t: torch.Tensor, dev, name: str = "rows") -> Tuple[int, int]:
+    """(pointer, B) of an int32 [B] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be an int32 tensor [B]")
+    n = t.shape[0]
+    _need(t, name, torch.int32, (n,), dev)
+    return t.data_ptr(), n
 
 
 def kda_kv_extend(cache: KdaKvCache, rows, n_tokens: Union[int, torch.Tensor], workspace=None, stream=None) -> None:
     """Pages and length for n_tokens (an int, or int32 [B]) more tokens of each row in rows (int32 [B],
     distinct), once per step for all layers; a partly filled last page that others share is copied."""
-    st, dev, B = cache.c_struct(), cache.device, _batch(rows)
-    pr = _ints(rows, "rows", B, dev)
+    _, st, _, dev = cache._struct()
+    pr, B = _rows(rows, dev)
     pn, n = (None, int(n_tokens)) if not isinstance(n_tokens, torch.Tensor) else (_ints(n_tokens, "n_tokens", B, dev), 0)
-    ws, nb = cache._workspace("kv_ws", workspace)
-    _call(dev, _lib.kda_kv_extend, ctypes.byref(st), pr, pn, n, B, ws, nb, _stream(stream, dev))
+    ws, nb = cache._workspace("_kv_ws", workspace)
+    _call(dev, _lib.kda_kv_extend, st, pr, pn, n, B, ws, nb, _stream(stream, dev))
 
 
 def kda_kv_truncate(cache: KdaKvCache, rows, new_lens, workspace=None, stream=None) -> None:
     """Cuts each row to new_lens (int32 [B]) tokens; 0 frees it.  Drafts that were not accepted."""
-    st, dev, B = cache.c_struct(), cache.device, _batch(rows)
-    ws, nb = cache._workspace("kv_ws", workspace)
-    _call(dev, _lib.kda_kv_truncate, ctypes.byref(st), _ints(rows, "rows", B, dev), _ints(new_lens, "new_lens", B, dev), B,
-          ws, nb, _stream(stream, dev))
+    _, st, _, dev = cache._struct()
+    pr, B = _rows(rows, dev)
+    ws, nb = cache._workspace("_kv_ws", workspace)
+    _call(dev, _lib.kda_kv_truncate, st, pr, _ints(new_lens, "new_lens", B, dev), B, ws, nb, _stream(stream, dev))
 
 
 def kda_kv_fork(cache: KdaKvCache, src_rows, dst_rows, workspace=None, stream=None) -> None:
     """Each dst row gives its pages back and shares all pages of its src row (int32 [n] both)."""
-    st, dev, n = cache.c_struct(), cache.device, _batch(src_rows)
-    ws, nb = cache._workspace("kv_ws", workspace)
-    _call(dev, _lib.kda_kv_fork, ctypes.byref(st), _ints(src_rows, "src_rows", n, dev), _ints(dst_rows, "dst_rows", n, dev), n,
-          ws, nb, _stream(stream, dev))
+    _, st, _, dev = cache._struct()
+    ps, n = _rows(src_rows, dev, "src_rows")
+    ws, nb = cache._workspace("_kv_ws", workspace)
+    _call(dev, _lib.kda_kv_fork, st, ps, _ints(dst_rows, "dst_rows", n, dev), n, ws, nb, _stream(stream, dev))
 
 
 def kda_kv_compact(cache: KdaKvCache, remap=None, workspace=None, stream=None) -> torch.Tensor:
     """Moves the pages in use to the lowest ids; returns the new id of each page (int32 [pages], -1:
     free before)."""
-    st, dev = cache.c_struct(), cache.device
+    _, st, _, dev = cache._struct()
     if remap is None:
         remap = torch.empty(cache.num_pages, dtype=torch.int32, device=dev)
-    ws, nb = cache._workspace("kv_ws", workspace)
-    _call(dev, _lib.kda_kv_compact, ctypes.byref(st), _ints(remap, "remap", cache.num_pages, dev), ws, nb, _stream(stream, dev))
+    ws, nb = cache._workspace("_kv_ws", workspace)
+    _call(dev, _lib.kda_kv_compact, st, _ints(remap, "remap", cache.num_pages, dev), ws, nb, _stream(stream, dev))
     return remap
 
 
-def _tokens(t: torch.Tensor, name: str, packed: bool, heads: Optional[int], D: int, dev) -> _Layout:
+def _tokens(t: torch.Tensor, name: str, packed: bool, heads: Optional[int], cache: KdaKvCache) -> _Layout:
     """Layout of [B, T, heads, D] or, packed, [N, heads, D]: any strides, the last dimension contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    D, dev = cache.head_dim, cache.device
     if t.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 or float16")
+    if cache.k.dtype != torch.float8_e4m3fn and cache.k.dtype != t.dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, the cache holds {cache.k.dtype}")
     n = t.shape
     if len(n) != (3 if packed else 4) or n[-1] != D or (heads is not None and n[-2] != heads):
         raise ValueError(f"{name}: shape {tuple(n)}, expected {'[N' if packed else '[B, T'}, "
@@ -210,50 +229,76 @@ def _tokens(t: torch.Tensor, name: str, packed: bool, heads: Optional[int], D: i
     return _Layout(_TYPES[t.dtype], 0 if packed or n[0] == 1 else st[0], 0 if n[-3] == 1 else st[-3], 0 if n[-2] == 1 else st[-2])
 
 
+def _plan(cache: KdaKvCache, key, make):
+    """What `make` works out for calls of this form (types, shapes, strides): checked and built at the
+    first one, kept with the cache, a few hundred at most."""
+    plans = cache.__dict__.get("_plans")
+    if plans is None:
+        plans = cache.__dict__["_plans"] = {}
+    got = plans.get(key)
+    if got is None:
+        if len(plans) >= 512:
+            plans.clear()
+        got = plans[key] = make()
+    return got
+
+
 def kda_kv_append(cache: KdaKvCache, layer: int, rows, k, v, cu_seqlens=None, n_tokens=None, stream=None) -> None:
     """Writes the new keys and values of a layer into their pages (after kda_kv_extend).  k, v are
     [B, T, Hkv, D], or packed [N, Hkv, D] with cu_seqlens int32 [B+1]; without it a packed [N, Hkv, D]
     holds N / B tokens of each row.  n_tokens int32 [B]: the first n of the T tokens count."""
-    st, dev, B = cache.c_struct(), cache.device, _batch(rows)
-    packed = k.dim() == 3
-    kl = _tokens(k, "k", packed, cache.Hkv, cache.head_dim, dev)
-    vl = _tokens(v, "v", packed, cache.Hkv, cache.head_dim, dev)
-    if k.shape != v.shape:
-        raise ValueError(f"k and v have shapes {tuple(k.shape)} and {tuple(v.shape)}")
-    pc = None
-    if cu_seqlens is not None:
-        if not packed:
-            raise ValueError("cu_seqlens goes with packed k and v [N, Hkv, D]")
-        pc, T = _ints(cu_seqlens, "cu_seqlens", B + 1, dev), k.shape[0]
-    elif packed:
-        if B and k.shape[0] % B:
-            raise ValueError(f"{k.shape[0]} packed tokens are no multiple of {B} rows: pass cu_seqlens")
-        T = k.shape[0] // B if B else 0
-        kl.seq_stride, vl.seq_stride = T * kl.token_stride, T * vl.token_stride
-    else:
-        if k.shape[0] != B:
-            raise ValueError(f"k: {k.shape[0]} sequences, rows has {B}")
-        T = k.shape[1]
+    _, st, _, dev = cache._struct()
+    pr, B = _rows(rows, dev)
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+
+    def make():
+        packed = k.dim() == 3
+        kl, vl = _tokens(k, "k", packed, cache.Hkv, cache), _tokens(v, "v", packed, cache.Hkv, cache)
+        if k.shape != v.shape:
+            raise ValueError(f"k and v have shapes {tuple(k.shape)} and {tuple(v.shape)}")
+        if cu_seqlens is not None:
+            if not packed:
+                raise ValueError("cu_seqlens goes with packed k and v [N, Hkv, D]")
+            T = k.shape[0]
+        elif packed:
+            if B and k.shape[0] % B:
+                raise ValueError(f"{k.shape[0]} packed tokens are no multiple of {B} rows: pass cu_seqlens")
+            T = k.shape[0] // B if B else 0
+            kl.seq_stride, vl.seq_stride = T * kl.token_stride, T * vl.token_stride
+        else:
+            if k.shape[0] != B:
+                raise ValueError(f"k: {k.shape[0]} sequences, rows has {B}")
+            T = k.shape[1]
+        return T, ctypes.byref(kl), ctypes.byref(vl)
+
+    T, kl, vl = _plan(cache, ("append", B, cu_seqlens is None, k.dtype, v.dtype, k.device, v.device, k.shape, v.shape, k.stride(), v.stride()), make)
+    pc = None if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", B + 1, dev)
     pn = None if n_tokens is None else _ints(n_tokens, "n_tokens", B, dev)
-    _call(dev, _lib.kda_kv_append, ctypes.byref(st), layer, _ints(rows, "rows", B, dev), B, T, pn, pc, k.data_ptr(),
-          ctypes.byref(kl), v.data_ptr(), ctypes.byref(vl), _stream(stream, dev))
+    _call(dev, _lib.kda_kv_append, st, layer, pr, B, T, pn, pc, k.data_ptr(), kl, v.data_ptr(), vl, _stream(stream, dev))
 
 
 def _attn(cache: KdaKvCache, q, packed: bool, scale, window, sinks, out, lse, return_lse):
     """Descriptor, output and lse of an attention call."""
-    dev, D = cache.device, cache.head_dim
-    ql = _tokens(q, "q", packed, None, D, dev)
-    if cache.k.dtype != torch.float8_e4m3fn and cache.k.dtype != q.dtype:
-        raise TypeError(f"q: dtype {q.dtype}, the cache holds {cache.k.dtype}")
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    shape = q.shape
+
+    def make():
+        ql = _tokens(q, "q", packed, None, cache)
+        D = cache.head_dim
+        return ctypes.byref(_Desc(shape[-2], 1.0 / math.sqrt(D) if scale is None else float(scale), int(window), int(sinks), ql))
+
+    desc = _plan(cache, ("attn", packed, scale, window, sinks, q.dtype, q.device, shape, q.stride()), make)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = q.new_empty(shape)
     else:
-        _need(out, "out", q.dtype, q.shape, dev)
+        _need(out, "out", q.dtype, shape, q.device)
     if lse is not None:
-        _need(lse, "lse", torch.float32, q.shape[:-1], dev)
+        _need(lse, "lse", torch.float32, shape[:-1], q.device)
     elif return_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    desc = _Desc(q.shape[-2], 1.0 / math.sqrt(D) if scale is None else float(scale), int(window), int(sinks), ql)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
     return desc, out, lse
 
 
@@ -264,14 +309,15 @@ def kda_attn_decode(cache: KdaKvCache, layer: int, rows, q, scale: Optional[floa
     Causal, or with a sliding window and sinks first tokens that stay visible.  n_tokens int32 [B]: only
     the first n of the T tokens count (entries past them are left as they were).  Returns out, or
     (out, lse f32 [B, T, Hq]) where lse is given or return_lse is set."""
-    st, dev, B = cache.c_struct(), cache.device, _batch(rows)
+    _, st, _, dev = cache._struct()
+    pr, B = _rows(rows, dev)
     desc, out, lse = _attn(cache, q, False, scale, window, sinks, out, lse, return_lse)
     if q.shape[0] != B:
         raise ValueError(f"q: {q.shape[0]} sequences, rows has {B}")
     pn = None if n_tokens is None else _ints(n_tokens, "n_tokens", B, dev)
-    ws, nb = cache._workspace("attn_ws", workspace)
-    _call(dev, _lib.kda_attn_decode, ctypes.byref(st), layer, ctypes.byref(desc), _ints(rows, "rows", B, dev), B, q.shape[1], pn,
-          q.data_ptr(), out.data_ptr(), _ptr(lse), ws, nb, _stream(stream, dev))
+    ws, nb = cache._workspace("_attn_ws", workspace)
+    _call(dev, _lib.kda_attn_decode, st, layer, desc, pr, B, q.shape[1], pn, q.data_ptr(), out.data_ptr(), _ptr(lse), ws, nb,
+          _stream(stream, dev))
     return out if lse is None else (out, lse)
 
 
@@ -281,20 +327,22 @@ def kda_attn_prefill(cache: KdaKvCache, layer: int, rows, cu_seqlens, max_len: i
     """Attention of packed new tokens: sequence b is rows cu_seqlens[b]..cu_seqlens[b+1]-1 of q [N, Hq, D],
     the last tokens of cache row rows[b]; max_len bounds every count (host int, no device read).
     Returns out, or (out, lse f32 [N, Hq]) where lse is given or return_lse is set."""
-    st, dev, B = cache.c_struct(), cache.device, _batch(rows)
+    _, st, _, dev = cache._struct()
+    pr, B = _rows(rows, dev)
     desc, out, lse = _attn(cache, q, True, scale, window, sinks, out, lse, return_lse)
-    ws, nb = cache._workspace("attn_ws", workspace)
-    _call(dev, _lib.kda_attn_prefill, ctypes.byref(st), layer, ctypes.byref(desc), _ints(rows, "rows", B, dev), B,
-          _ints(cu_seqlens, "cu_seqlens", B + 1, dev), q.shape[0], int(max_len), q.data_ptr(), out.data_ptr(), _ptr(lse),
+    pc = _ints(cu_seqlens, "cu_seqlens", B + 1, dev)
+    ws, nb = cache._workspace("_attn_ws", workspace)
+    _call(dev, _lib.kda_attn_prefill, st, layer, desc, pr, B, pc, q.shape[0], int(max_len), q.data_ptr(), out.data_ptr(), _ptr(lse),
           ws, nb, _stream(stream, dev))
     return out if lse is None else (out, lse)
 
 
 def kda_kv_get_error(cache: KdaKvCache, stream=None) -> int:
     """Reads and clears the cache's device error word (synchronises the stream)."""
-    st, dev, v = cache.c_struct(), cache.device, ctypes.c_int32(0)
+    _, st, _, dev = cache._struct()
+    v = ctypes.c_int32(0)
     with torch.cuda.device(dev):
-        r = _lib.kda_kv_get_error(ctypes.byref(st), ctypes.byref(v), _stream(stream, dev))
+        r = _lib.kda_kv_get_error(st, ctypes.byref(v), _stream(stream, dev))
     if r not in (KDA_OK, KDA_ERR_DEVICE):
         _raise(r)
     return int(v.value)
