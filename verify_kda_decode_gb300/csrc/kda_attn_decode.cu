@@ -65,17 +65,24 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
     return v;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NB>
 struct Cfg {
     static constexpr int ES = FP8 ? 1 : 2;
     static constexpr int RB = D * ES;                     // bytes of a key
     static constexpr int CH = RB / 16;                    // its 16-byte chunks
     static constexpr int STAGE = 2 * kStep * RB;          // keys, then values
-    static constexpr int NS = 24576 / STAGE > 8 ? 8 : 24576 / STAGE;
+    // CTAs of an SM: as many as the accumulators (D NB / 4 registers) leave room for.  A warp's step is a
+    // chain of latencies (scores, maximum over lanes, exponentials, product), which other warps cover:
+    // with two CTAs everywhere an E4M3 cache (64 x 4096 tokens, 8 heads) took 153 us, OCC4_E4M3.
+    static constexpr int OCC = D * NB >= 512 ? 2 : (RB == 256 || D * NB >= 256) ? 3 : 4;
+    static constexpr bool Q_SMEM = NB > 1;                // queries in shared memory instead of registers
+    static constexpr int Q_BYTES = Q_SMEM ? NB * 8 * D * 2 : 0;
+    static constexpr int NS_FIT = (220 * 1024 / OCC - 2048 - Q_BYTES) / (kWarps * STAGE);
+    static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;    // stages of a warp's ring
     static constexpr int RING = kWarps * NS * STAGE;
     // the pieces of a unit are merged in the ring's place
-    static constexpr int merge_bytes(int nb) { return kWarps * 8 * nb * (D + 2) * 4; }
-    static constexpr int smem(int nb) { return RING > merge_bytes(nb) ? RING : merge_bytes(nb); }
+    static constexpr int MERGE = kWarps * 8 * NB * (D + 2) * 4;
+    static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + Q_BYTES;
     // chunk c of row r is stored at chunk c ^ swz(r): conflict-free for the fragment loads
     // (K: eight lanes read four chunks of two rows; V: two chunks of four even rows)
     static __device__ __forceinline__ int swz_k(int r) { return CH >= 8 ? 4 * (r & 1) : 0; }
@@ -85,28 +92,45 @@ struct Cfg {
 };
 
 struct Partials {   // workspace: counters, then for each CTA two slots of (m, l, O)
-    int *count;
+    int *count, *group;   // [kMaxCtas] of units by first CTA, [2 kMaxCtas] of groups by first slot
     float *data;
+    static constexpr size_t kCounters = 3 * kMaxCtas;
     static constexpr size_t slot_floats(int D) { return (size_t)kMaxRows * (D + 2); }
     __device__ float *slot(int s, int D) const { return data + (size_t)s * slot_floats(D); }
 };
 
-template <int D, typename Q, bool FP8, int NB>
-__global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const AttnParams p)
+__device__ __forceinline__ float ex2(float x)
 {
-    using C = Cfg<D, FP8>;
-    using P = std::conditional_t<FP8, Half, Q>;   // type of the second product
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Runs of tiles are counted in 64 bits (rows that share pages can hold more keys than memory); the
+// divisions take the 32-bit path whenever the numbers allow it.
+__device__ __forceinline__ long long div_pos(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+template <int D, typename Q, bool FP8, int NB>
+__global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decode_kernel(const AttnParams p)
+{
+    using C = Cfg<D, FP8, NB>;
+    using P = std::conditional_t<FP8, Half, Q>;   // type of both products: E4M3 codes are exact halves
+    constexpr int kSeqs = 256;                    // sequences whose (row, length, tokens) are kept on chip
     constexpr int MT = D / 16;                    // accumulator blocks (16 head dims)
     constexpr int ROWS = 8 * NB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long sh_prefix, sh_warp[kWarps];
-    __shared__ int sh_b, sh_last;
+    __shared__ int sh_b, sh_last, sh_seq[3][kSeqs];
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, cc = lane & 3;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
     Partials part;
     part.count = reinterpret_cast<int *>(p.ws);
-    part.data = reinterpret_cast<float *>(p.ws + kMaxCtas * sizeof(int));
+    part.group = part.count + kMaxCtas;
+    part.data = reinterpret_cast<float *>(p.ws + Partials::kCounters * sizeof(int));
 
     grid_dependency_wait();
 
@@ -123,7 +147,17 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
     const int per = (p.B + kThreads - 1) / kThreads, b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
     long long mine = 0;
     int kt, mt;
-    for (int b = b_lo; b < b_hi; b++) mine += tiles_of(load_seq(b, blockIdx.x == 0), kt, mt);
+    for (int b = b_lo; b < b_hi; b++) {
+        const SeqInfo s = load_seq(b, blockIdx.x == 0);
+        if (b < kSeqs) sh_seq[0][b] = s.row, sh_seq[1][b] = s.len, sh_seq[2][b] = s.ok ? s.n : 0;
+        mine += tiles_of(s, kt, mt);
+    }
+    auto seq_of = [&](int b) {   // after the barrier below
+        if (b >= kSeqs) return load_seq(b, false);
+        SeqInfo s;
+        s.row = sh_seq[0][b], s.len = sh_seq[1][b], s.n = sh_seq[2][b], s.ok = true;
+        return s;
+    };
     long long before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -139,13 +173,13 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
         if (i < w) before += sh_warp[i];
         total += sh_warp[i];
     }
-    const long long chunk = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+    const long long chunk = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
     const long long begin = blockIdx.x * chunk, end = min(total, begin + chunk);
     if (begin >= end) return;
     if (begin >= before && begin < before + mine) {
         long long at = before;
         for (int b = b_lo; b < b_hi; b++) {
-            const long long n = tiles_of(load_seq(b, false), kt, mt);
+            const long long n = tiles_of(seq_of(b), kt, mt);
             if (begin < at + n) {
                 sh_b = b;
                 sh_prefix = at;
@@ -157,22 +191,23 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
     __syncthreads();
     int b = sh_b;
     long long prefix = sh_prefix;
-    SeqInfo seq = load_seq(b, false);
+    SeqInfo seq = seq_of(b);
     long long seq_tiles = tiles_of(seq, kt, mt);
 
-    const uint32_t ring = smem_u32(smem) + w * (C::NS * C::STAGE);
-    uint8_t *ring_p = smem + w * (C::NS * C::STAGE);
-    float *mg = reinterpret_cast<float *>(smem);          // merge buffer: O [warp][ROWS][D], m, l [warp][ROWS]
+    uint2 *q_sm = reinterpret_cast<uint2 *>(smem);        // queries, [NB][D / 16][32 lanes]
+    uint8_t *ring_p = smem + C::Q_BYTES + w * (C::NS * C::STAGE);
+    const uint32_t ring = smem_u32(ring_p), q_at = smem_u32(smem) + lane * 8;
+    float *mg = reinterpret_cast<float *>(smem + C::Q_BYTES);          // merge buffer: O [warp][ROWS][D], m, l [warp][ROWS]
     float *mg_m = mg + kWarps * ROWS * D, *mg_l = mg_m + kWarps * ROWS;
 
     long long at = begin;
     while (at < end) {
         while (at >= prefix + seq_tiles) {   // next sequence with work (there is one: at < total)
             prefix += seq_tiles;
-            seq = load_seq(++b, false);
+            seq = seq_of(++b);
             seq_tiles = tiles_of(seq, kt, mt);
         }
-        const int local = (int)((at - prefix) / kt);
+        const int local = (int)div_pos(at - prefix, kt);
         const int h = local / mt, mb = local % mt;
         const long long u0 = prefix + (long long)local * kt;              // the unit's tiles [u0, u0 + kt)
         const int ta = (int)(at - u0), tb = (int)min((long long)kt, end - u0);
@@ -183,25 +218,68 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
         const size_t head_bytes = (size_t)c.ps * C::RB;
         const size_t layer_off = (size_t)p.layer * c.pages;
 
-        // queries: rows nb * 8 + g, the elements this thread multiplies
-        uint32_t qf[NB][D / 16][2];
+        // queries: rows nb * 8 + g, the elements this thread multiplies.  With an E4M3 cache the products are
+        // taken in halves: a bfloat16 row is brought to a maximum in [1, 2) by a power of two first (exact
+        // but for elements under 2^-14 of it, whose error stays under 2^-25 of it)
+        uint32_t qf[C::Q_SMEM ? 1 : D / 16][2];
+        float sc[NB][2];      // scale of rows 2 cc, 2 cc + 1, in log2 units
+        int row_pos[NB][2];   // and their tokens' positions
+        const float sc_head = p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = nb * 8 + g;
-            const int t = (mb * ROWS + r) / p.G, hq = h * p.G + (mb * ROWS + r) % p.G;
+            const int t = (mb * ROWS + r) / p.G, hq = h * p.G + (mb * ROWS + r) - t * p.G;
             const uint16_t *src = p.q + b * p.ql.seq + t * p.ql.token + hq * p.ql.head;
+            uint4 x[D / 32];
 #pragma unroll
             for (int j = 0; j < D / 32; j++) {
                 // 16-bit cache: chunk cc + 4 j of 8 elements; E4M3: 16-element chunks, this is half (j & 1) of chunk cc + 4 (j / 2)
                 const int e = FP8 ? 16 * (cc + 4 * (j >> 1)) + 8 * (j & 1) : 8 * (cc + 4 * j);
-                const uint4 x = r < n_rows ? __ldg(reinterpret_cast<const uint4 *>(src + e)) : make_uint4(0, 0, 0, 0);
-                qf[nb][2 * j][0] = x.x;
-                qf[nb][2 * j][1] = x.y;
-                qf[nb][2 * j + 1][0] = x.z;
-                qf[nb][2 * j + 1][1] = x.w;
+                x[j] = r < n_rows ? __ldg(reinterpret_cast<const uint4 *>(src + e)) : make_uint4(0, 0, 0, 0);
+            }
+            float up = 1.f;
+            if constexpr (FP8 && !Q::is_half) {
+                uint32_t mx = 0;   // largest magnitude's bits
+#pragma unroll
+                for (int j = 0; j < D / 32; j++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint32_t y = (&x[j].x)[i];
+                        mx = max(mx, max(y & 0x7fffu, (y >> 16) & 0x7fffu));
+                    }
+                mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
+                mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
+                const int ex = (int)(mx >> 7);                          // biased exponent
+                const int e = ex == 255 ? 0 : min(max(ex, 1) - 127, 126);   // infinite rows stay as they are
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                up = __uint_as_float((uint32_t)max(127 + e, 1) << 23);
+#pragma unroll
+                for (int j = 0; j < D / 32; j++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        uint32_t &y = (&x[j].x)[i];
+                        y = Half::pack(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xffff0000u) * down);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                sc[nb][i] = sc_head * (FP8 && !Q::is_half ? __shfl_sync(~0u, up, 4 * (2 * cc + i)) : 1.f);
+                row_pos[nb][i] = p0 + (mb * ROWS + nb * 8 + 2 * cc + i) / p.G;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; j++) {
+                if constexpr (C::Q_SMEM) {
+                    if (w == (nb & 3)) {
+                        q_sm[(nb * (D / 16) + 2 * j) * 32 + lane] = make_uint2(x[j].x, x[j].y);
+                        q_sm[(nb * (D / 16) + 2 * j + 1) * 32 + lane] = make_uint2(x[j].z, x[j].w);
+                    }
+                } else {
+                    qf[2 * j][0] = x[j].x, qf[2 * j][1] = x[j].y;
+                    qf[2 * j + 1][0] = x[j].z, qf[2 * j + 1][1] = x[j].w;
+                }
             }
         }
-        const float sc = p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
+        if constexpr (C::Q_SMEM) __syncthreads();
 
         float acc[MT][NB][4];
 #pragma unroll
@@ -268,9 +346,20 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
             st_out = st_out + 1 == C::NS ? 0 : st_out + 1;
             if (step_used(k0) && !(bad >> stage & 1)) {
                 const uint32_t kb = ring + stage * C::STAGE, vb = kb + kStep * C::RB;
-                float s[NB][4];
+                float s[NB][4], s2[NB][4];   // two chains of products, added at the end
 #pragma unroll
-                for (int nb = 0; nb < NB; nb++) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) s[nb][i] = s2[nb][i] = 0.f;
+                auto qk = [&](int kb_, const uint32_t *a) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++) {
+                        uint2 q;
+                        if constexpr (C::Q_SMEM) q = lds64(q_at + (nb * (D / 16) + kb_) * 256);
+                        else q = make_uint2(qf[kb_][0], qf[kb_][1]);
+                        mma16816<P>(kb_ & 1 ? s2[nb] : s[nb], a, q.x, q.y);
+                    }
+                };
 #pragma unroll
                 for (int j = 0; j < C::CH / 4; j++) {
                     const uint4 x = lds128(kb + g * C::RB + (((cc + 4 * j) ^ C::swz_k(g)) * 16));
@@ -279,16 +368,14 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
                     if constexpr (FP8) {
 #pragma unroll
                         for (int u = 0; u < 4; u++) {
-                            const uint32_t a[4] = {e4m3x2_as<Q>(xs[u], 0), e4m3x2_as<Q>(ys[u], 0), e4m3x2_as<Q>(xs[u], 1), e4m3x2_as<Q>(ys[u], 1)};
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++) mma16816<Q>(s[nb], a, qf[nb][4 * j + u][0], qf[nb][4 * j + u][1]);
+                            const uint32_t a[4] = {e4m3x2_half2(xs[u], 0), e4m3x2_half2(ys[u], 0), e4m3x2_half2(xs[u], 1), e4m3x2_half2(ys[u], 1)};
+                            qk(4 * j + u, a);
                         }
                     } else {
 #pragma unroll
                         for (int u = 0; u < 2; u++) {
                             const uint32_t a[4] = {xs[2 * u], ys[2 * u], xs[2 * u + 1], ys[2 * u + 1]};
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++) mma16816<Q>(s[nb], a, qf[nb][2 * j + u][0], qf[nb][2 * j + u][1]);
+                            qk(2 * j + u, a);
                         }
                     }
                 }
@@ -298,11 +385,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
                 for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        s[nb][i] *= sc;
-                        if (!all) {
-                            const int tok = (mb * ROWS + nb * 8 + 2 * cc + (i & 1)) / p.G;
-                            if (!key_visible(k0 + g + 8 * (i >> 1), p0 + tok, W, S)) s[nb][i] = -INFINITY;
-                        }
+                        s[nb][i] = (s[nb][i] + s2[nb][i]) * sc[nb][i & 1];
+                        if (!all && !key_visible(k0 + g + 8 * (i >> 1), row_pos[nb][i & 1], W, S)) s[nb][i] = -INFINITY;
                     }
                 uint32_t pf[NB][2];
                 bool grown = false;
@@ -317,10 +401,10 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
                         const float m_new = fmaxf(row_m[nb][i], mx);
                         const float base = m_new == -INFINITY ? 0.f : m_new;   // a row that has seen no key yet
                         grown |= m_new > row_m[nb][i];
-                        alpha[nb][i] = exp2f(row_m[nb][i] - base);
+                        alpha[nb][i] = ex2(row_m[nb][i] - base);
                         row_m[nb][i] = m_new;
-                        s[nb][i] = exp2f(s[nb][i] - base);
-                        s[nb][i + 2] = exp2f(s[nb][i + 2] - base);
+                        s[nb][i] = ex2(s[nb][i] - base);
+                        s[nb][i + 2] = ex2(s[nb][i + 2] - base);
                         row_l[nb][i] = row_l[nb][i] * alpha[nb][i] + (s[nb][i] + s[nb][i + 2]);
                     }
                     // P is rounded to the product's 16-bit type (relative error 2^-9 or 2^-12, as the
@@ -404,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
             }
         __syncthreads();
 
-        const int f = (int)(u0 / chunk), l = (int)((u0 + kt - 1) / chunk);   // CTAs that hold the unit's pieces
+        const int f = (int)div_pos(u0, chunk), l = (int)div_pos(u0 + kt - 1, chunk);   // CTAs that hold the unit's pieces
         const float v_scale = FP8 ? c.v_scale[p.layer * c.Hkv + h] : 1.f;
         auto store = [&](int r, int d, float4 o, float l_sum, float m) {   // 4 outputs of a row
             const int t = (mb * ROWS + r) / p.G, hq = h * p.G + (mb * ROWS + r) % p.G;
@@ -424,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kWarps; i++) {
-                const float a = exp2f(mg_m[i * ROWS + r] - base);
+                const float a = ex2(mg_m[i * ROWS + r] - base);
                 const float4 y = *reinterpret_cast<const float4 *>(&mg[(i * ROWS + r) * D + d]);
                 ls += a * mg_l[i * ROWS + r];
                 o.x += a * y.x, o.y += a * y.y, o.z += a * y.z, o.w += a * y.w;
@@ -439,33 +523,61 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_decode_kernel(const Attn
             }
         }
         if (f != l) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int done = atomicAdd(&part.count[f], 1);
-                sh_last = done == l - f;
-                if (done == l - f) part.count[f] = 0;   // ready for the next call
-                __threadfence();
-            }
-            __syncthreads();
-            if (sh_last) {
-                const int n = l - f + 1;
+            // pieces [i0, i1) (i-th piece: the unit's slot of CTA f + i, one in `step` of them) in order
+            auto join = [&](int i0, int i1, int step, bool last) {
+                float *to = part.slot(2 * (f + i0) + (i0 == 0), D);
                 for (int x = tid; x < n_rows * (D / 4); x += kThreads) {
                     const int r = x / (D / 4), d = x % (D / 4) * 4;
                     float m = -INFINITY, ls = 0.f;
 #pragma unroll 8
-                    for (int i = 0; i < n; i++) m = fmaxf(m, __ldcg(part.slot(2 * (f + i) + (i == 0), D) + r));
+                    for (int i = i0; i < i1; i += step) m = fmaxf(m, __ldcg(part.slot(2 * (f + i) + (i == 0), D) + r));
                     const float base = m == -INFINITY ? 0.f : m;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-                    for (int i = 0; i < n; i++) {
+                    for (int i = i0; i < i1; i += step) {
                         const float *q = part.slot(2 * (f + i) + (i == 0), D);
-                        const float a = exp2f(__ldcg(q + r) - base);
+                        const float a = ex2(__ldcg(q + r) - base);
                         const float4 y = __ldcg(reinterpret_cast<const float4 *>(q + 2 * kMaxRows + r * D + d));
                         ls += a * __ldcg(q + kMaxRows + r);
                         o.x += a * y.x, o.y += a * y.y, o.z += a * y.z, o.w += a * y.w;
                     }
-                    store(r, d, o, ls, m);
+                    if (last) store(r, d, o, ls, m);
+                    else {
+                        __stcg(reinterpret_cast<float4 *>(to + 2 * kMaxRows + r * D + d), o);
+                        // the row's (m, l) are still read by its other threads: kept apart until all are done
+                        if (d == 0) mg_m[r] = m, mg_l[r] = ls;
+                    }
+                }
+                if (!last) {
+                    __syncthreads();
+                    if (tid < n_rows) {
+                        __stcg(to + tid, mg_m[tid]);
+                        __stcg(to + kMaxRows + tid, mg_l[tid]);
+                    }
+                }
+            };
+            // true in the CTA that is the `n`-th to come to this counter, which is then ready for the next call
+            auto last_of = [&](int *counter, int n) {
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    const int done = atomicAdd(counter, 1);
+                    sh_last = done == n - 1;
+                    if (sh_last) *counter = 0;
+                    __threadfence();
+                }
+                __syncthreads();
+                return sh_last != 0;
+            };
+            // up to 16 pieces are joined at once, more in groups of 8 first
+            const int n = l - f + 1;
+            if (n <= 16) {
+                if (last_of(&part.count[f], n)) join(0, n, 1, true);
+            } else {
+                const int i0 = ((int)blockIdx.x - f) & ~7, i1 = min(n, i0 + 8);
+                if (last_of(&part.group[2 * (f + i0) + (i0 == 0)], i1 - i0)) {
+                    join(i0, i1, 1, false);
+                    if (last_of(&part.count[f], (n + 7) / 8)) join(0, n, 8, true);
                 }
             }
         }
@@ -478,7 +590,8 @@ template <int D, typename Q, bool FP8, int NB>
 cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr int smem = Cfg<D, FP8>::smem(NB);
+    constexpr int smem = Cfg<D, FP8, NB>::SMEM;
+    static_assert(Cfg<D, FP8, NB>::NS >= 2 && Cfg<D, FP8, NB>::NS <= 32, "a ring of two stages at least");
     int resident = 0;
     const cudaError_t e = setup.get(kda_attn_decode_kernel<D, Q, FP8, NB>, kThreads, smem, 0, &resident);
     if (e != cudaSuccess) return e;
@@ -506,7 +619,7 @@ cudaError_t launch_types(const AttnParams &p, cudaStream_t stream)
 
 }  // namespace
 
-size_t attn_decode_workspace(int D) { return kMaxCtas * sizeof(int) + 2 * kMaxCtas * Partials::slot_floats(D) * sizeof(float); }
+size_t attn_decode_workspace(int D) { return Partials::kCounters * sizeof(int) + 2 * kMaxCtas * Partials::slot_floats(D) * sizeof(float); }
 
 cudaError_t launch_attn_decode(const AttnParams &p, cudaStream_t stream)
 {
