@@ -94,7 +94,8 @@ struct Cfg {
 struct Partials {   // workspace: counters, then for each CTA two slots of (m, l, O)
     int *count, *group;   // [kMaxCtas] of units by first CTA, [2 kMaxCtas] of groups by first slot
     float *data;
-    static constexpr size_t kCounters = 3 * kMaxCtas;
+    static constexpr size_t kCounters = kAttnCounters;
+    static_assert(kCounters >= 3 * kMaxCtas, "units and groups");
     static constexpr size_t slot_floats(int D) { return (size_t)kMaxRows * (D + 2); }
     __device__ float *slot(int s, int D) const { return data + (size_t)s * slot_floats(D); }
 };

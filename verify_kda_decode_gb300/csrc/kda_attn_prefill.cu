@@ -13,9 +13,13 @@
 // tensor cores, or the 128 x 128 exponentials of each tile next to them.  Two halves, so that one
 // half's softmax runs while the tensor cores work on the other's products.
 //
+// Persistent: one CTA per SM takes (sequence, row tile, key head) units off a counter, the longest of a
+// causal prompt first, so that one unit's queries and keys are on their way while the last one's sums are
+// written (a CTA per unit spent 14 us of each unit outside its products).
+//
 // Roles: warps 0-3 and 4-7 are the softmax of the two halves (one thread per row), warps 8-11 copy
-// keys and values into a ring of shared-memory tiles, one lane of warp 12 issues every MMA (warps 13-15
-// only give their registers away).  Hand-over
+// keys and values into a ring of shared-memory tiles, warp 12 issues every MMA, warp 13 finds
+// the next unit (14 and 15 only give their registers away).  Hand-over
 // by mbarriers; a half's S tile also orders its previous P V (a commit covers every MMA issued before
 // it).  With few row tiles the key tiles are split over several CTAs whose partial (m, l, O) the last
 // one to finish joins in a fixed order.
@@ -38,20 +42,34 @@ namespace {
 constexpr int kHalf = 128, kRowsCta = 256, kKeys = 128;
 constexpr int kSoftmax = 256, kLoaders = 128, kThreads = kSoftmax + kLoaders + 128;
 // Registers of a thread: all start with 128 (512 threads, the whole file), then the softmax holds a row
-// of S at once, the loaders two fetches of E4M3 codes; 256 x 184 + 128 x 104 + 128 x 40 = 65536.
-constexpr int kRegs = 128, kRegsSoftmax = 184, kRegsLoad = 104, kRegsMma = 40;
-constexpr int kSlots = 4, kHalfBytes = kKeys * 128;   // a tile's 64 head dims: 128 rows of 128 bytes
+// of S at once, the loaders two fetches of E4M3 codes; 256 x 184 + 128 x 80 + 128 x 64 = 65536.
+constexpr int kRegs = 128, kRegsSoftmax = 184, kRegsLoad = 80, kRegsMma = 64;
+constexpr uint32_t kSlots = 4;
+constexpr int kHalfBytes = kKeys * 128;   // a tile's 64 head dims: 128 rows of 128 bytes
 constexpr int kMaxSplitCtas = 256;             // CTAs of a launch whose keys are split
 constexpr uint64_t kLimitNs = 2000000000ull;   // bound of every wait
+constexpr int kUnits = 2, kTable = 1024;       // units on their way to the roles; sequences whose tile counts are kept on chip
 constexpr float kGrow = 8.f;                   // log2 growth of the maximum that O is rescaled for
+
+// What a CTA works on: rows [r0, r0 + rows) of the n * G of a sequence, and key tiles [ta, tb) of their range.
+struct Unit {
+    int idx;               // its number: (row tile, key head, split), -1: no more
+    int row, h;            // cache row, key head
+    int c0, n, len;        // first packed token, new tokens, row length
+    int r0, rows, halves;
+    int p_first, p_last;   // positions of its first and last token
+    int ta, tb, pieces;    // pieces > 1: the keys are split
+};
 
 template <int D>
 struct Smem {
     uint8_t q[2][kHalf * D * 2];
     uint8_t kv[kSlots][kKeys * D * 2];
-    uint64_t q_full, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q_full, q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
+    Unit unit[kUnits];
+    int before[kTable + 1], warp_sum[16];   // row tiles of the sequences before each one
     uint32_t tmem;
-    int unit_b, unit_tile, c0, n, last;
+    int last;
     volatile int stop;
 };
 
@@ -102,6 +120,12 @@ __device__ __forceinline__ float ex2(float x)
 
 static_assert(kSoftmax * kRegsSoftmax + kLoaders * kRegsLoad + 128 * kRegsMma <= kThreads * kRegs, "setmaxnreg would wait forever");
 
+__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1)
+{
+    asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\tadd.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1));
+}
+
 // 32 tensor-memory columns of this warp's lanes.  Load and wait are one statement, so that nothing
 // that uses the registers can be placed between them.
 __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *r)
@@ -145,11 +169,6 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1)
-{
-    asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\tadd.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1));
-}
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -181,82 +200,136 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, 
         : "memory");
 }
 
-// What a CTA works on.
-struct Unit {
-    int row;               // cache row
-    int h;                 // key head
-    int b, c0, n, len;     // sequence, first packed token, new tokens, row length
-    int r0, rows;          // rows [r0, r0 + rows) of the sequence's n * G
-    int halves;
-    int ta, tb;            // key tiles of the range that this CTA takes
-};
-
+// Bounded wait: after two seconds, or when another role has given up, the CTA winds down.
 template <int D>
-__device__ __forceinline__ bool wait(Smem<D> &sm, uint64_t *bar, uint32_t parity, int *err)
+__device__ __forceinline__ bool wait_long(Smem<D> &sm, uint64_t *bar, uint32_t parity, int *err)
 {
-    if (mbar_wait_bounded(bar, parity, kLimitNs)) return true;
-    sm.stop = 1;
-    atomicOr(err, KDA_DEVERR_TIMEOUT);
+    const uint64_t t0 = globaltimer_ns();
+    while (!sm.stop) {
+        for (int i = 0; i < 64; i++)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > kLimitNs) {
+            sm.stop = 1;
+            atomicOr(err, KDA_DEVERR_TIMEOUT);
+        }
+    }
     return false;
 }
 // ... by all lanes of a warp, which agree on the outcome
 template <int D>
 __device__ __forceinline__ bool wait_warp(Smem<D> &sm, uint64_t *bar, uint32_t parity, int *err)
 {
-    return __all_sync(~0u, wait(sm, bar, parity, err));
+    for (int i = 0; i < 64; i++)   // the usual wait ends here, without a look at the clock
+        if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(~0u, wait_long(sm, bar, parity, err));
 }
 
-// ---- warp 12: products, in the order that lets one half's softmax run beside the other's products
-template <int D, typename Q>
-__device__ void issue_products(Smem<D> &sm, const Unit &u, uint32_t tmem, int *err)
+// A role's k-th unit, left by warp 13 in shared memory: null when there is no more (or a wait gave up).
+template <int D>
+__device__ __forceinline__ const Unit *unit_of(Smem<D> &sm, int k, int *err)
 {
-    const int n = u.tb - u.ta;
-    auto slot_wait = [&](int item) { return wait(sm, &sm.full[item % kSlots], (item / kSlots) & 1, err); };
-    auto qk = [&](int h, int item) {
-        const uint64_t ad = desc_sw128(smem_u32(sm.q[h]), 16u), bd = desc_sw128(smem_u32(sm.kv[item % kSlots]), 16u);
+    if (!wait_warp(sm, &sm.u_full[k % kUnits], (k / kUnits) & 1, err)) return nullptr;
+    const Unit *u = &sm.unit[k % kUnits];
+    return u->idx >= 0 ? u : nullptr;
+}
+// ... and that this warp is done with it.
+template <int D>
+__device__ __forceinline__ void unit_done(Smem<D> &sm, int k)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.u_empty[k % kUnits]);
+}
+
+// True in one lane, the same one at every call.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// ---- warp 12: products, in the order that lets one half's softmax run beside the other's products: P V of
+// a tile, then Q K^T of the half's next one (which overwrites P only after it is read: one thread's products
+// run in order).  The whole warp walks the loop, so that the descriptors stay in uniform registers, and
+// one lane issues.
+// `item`: ring items so far; `tiles`: key tiles so far of each half; `units`: units with products so far
+template <int D, typename Q, int HALVES>
+__device__ __forceinline__ bool issue_products(Smem<D> &sm, int n, uint32_t tmem, uint32_t &item, uint32_t *tiles, uint32_t &units, int *err)
+{
+    const uint64_t q_desc = desc_sw128(smem_u32(sm.q[0]), 16u), k_desc = desc_sw128(smem_u32(sm.kv[0]), 16u),
+                   v_desc = desc_sw128(smem_u32(sm.kv[0]), kHalfBytes);
+    constexpr uint32_t kTile = kKeys * D * 2 >> 4;   // a ring slot, a half's queries, in descriptor units
+    auto slot_wait = [&](uint32_t it) { return wait_warp(sm, &sm.full[it % kSlots], (it / kSlots) & 1, err); };
+    auto qk = [&](int h, uint32_t it, bool last_tile) {
+        const uint64_t ad = q_desc + h * kTile, bd = k_desc + (it % kSlots) * kTile;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; k++) {   // 16 head dims: 32 bytes further in the half's rows
-            const uint32_t step = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-            tc::mma(tmem + Cols<D>::s(h), ad + step, bd + step, idesc<Q>(kKeys), k > 0);
-        }
-        tc::commit(&sm.s_full[h]);
-    };
-    auto pv = [&](int h, int item, bool accumulate) {
-        const uint64_t bd = desc_sw128(smem_u32(sm.kv[item % kSlots]), kHalfBytes);
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; k++)   // 16 keys: two groups of 8 rows
-            mma_ts(tmem + Cols<D>::o(h), tmem + Cols<D>::p(h) + 8 * k, bd + k * (2048u >> 4), idesc<Q>(D) | (1u << 16), accumulate || k > 0);
-    };
-    if (!wait(sm, &sm.q_full, 0, err)) return;
-    if (!slot_wait(0)) return;
-    tc::fence_after_sync();
-    for (int h = 0; h < u.halves; h++) qk(h, 0);
-    tc::commit(&sm.empty[0]);
-    for (int i = 0; i < n; i++) {
-        if (!slot_wait(2 * i + 1)) return;
-        for (int h = 0; h < u.halves; h++) {
-            if (!wait(sm, &sm.p_full[h], i & 1, err)) return;
-            tc::fence_after_sync();
-            pv(h, 2 * i + 1, i > 0);
-            if (i + 1 == n) tc::commit(&sm.o_full[h]);
-            if (h + 1 == u.halves) tc::commit(&sm.empty[(2 * i + 1) % kSlots]);
-            if (i + 1 < n) {
-                if (h == 0) {
-                    if (!slot_wait(2 * i + 2)) return;
-                    tc::fence_after_sync();
-                }
-                qk(h, 2 * i + 2);
-                if (h + 1 == u.halves) tc::commit(&sm.empty[(2 * i + 2) % kSlots]);
+            for (int k = 0; k < D / 16; k++) {   // 16 head dims: 32 bytes further in the half's rows
+                const uint32_t step = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                tc::mma(tmem + Cols<D>::s(h), ad + step, bd + step, idesc<Q>(kKeys), k > 0);
+            }
+            tc::commit(&sm.s_full[h]);
+            if (h + 1 == HALVES) {
+                tc::commit(&sm.empty[it % kSlots]);
+                if (last_tile) tc::commit(&sm.q_empty);
             }
         }
+    };
+    if (!wait_warp(sm, &sm.q_full, units & 1, err)) return false;
+    if (!slot_wait(item)) return false;
+    tc::fence_after_sync();
+#pragma unroll
+    for (int h = 0; h < HALVES; h++) qk(h, item, n == 1);
+    for (int i = 0; i < n; i++) {
+        const uint32_t it = item + 2 * i + 1;
+        if (!slot_wait(it)) return false;
+        const bool more = i + 1 < n;
+        if (more && !slot_wait(it + 1)) return false;
+#pragma unroll
+        for (int h = 0; h < HALVES; h++) {
+            const uint64_t bd = v_desc + (it % kSlots) * kTile;
+            if (!wait_warp(sm, &sm.p_full[h], (tiles[h] + i) & 1, err)) return false;
+            tc::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; k++)   // 16 keys: two groups of 8 rows
+                    mma_ts(tmem + Cols<D>::o(h), tmem + Cols<D>::p(h) + 8 * k, bd + k * (2048u >> 4), idesc<Q>(D) | (1u << 16), i > 0 || k > 0);
+                if (!more) tc::commit(&sm.o_full[h]);
+                if (h + 1 == HALVES) tc::commit(&sm.empty[it % kSlots]);
+            }
+            if (more) qk(h, it + 1, i + 2 == n);
+        }
+    }
+    item += 2 * n;
+    units++;
+#pragma unroll
+    for (int h = 0; h < HALVES; h++) tiles[h] += n;
+    return true;
+}
+
+template <int D, typename Q>
+__device__ void mma_role(Smem<D> &sm, uint32_t tmem, int *err)
+{
+    uint32_t item = 0, tiles[2] = {0, 0}, units = 0;
+    for (int k = 0; const Unit *u = unit_of(sm, k, err); k++) {
+        // (the reductions leave their results in uniform registers)
+        const int n = __reduce_max_sync(~0u, u->tb - u->ta);
+        const bool two = __all_sync(~0u, u->halves == 2);
+        unit_done(sm, k);
+        if (n == 0) continue;
+        if (!(two ? issue_products<D, Q, 2>(sm, n, tmem, item, tiles, units, err)
+                                             : issue_products<D, Q, 1>(sm, n, tmem, item, tiles, units, err)))
+            return;
     }
 }
 
-// ---- warps 8-11: keys and values of tile i as ring items 2 i and 2 i + 1
+// ---- warps 8-11: a unit's queries, then keys and values of tile i as ring items 2 i and 2 i + 1
+// (`item`: ring items so far, `units`: units so far)
 template <int D, typename Q, bool FP8>
-__device__ void load_tiles(Smem<D> &sm, const Args &args, const Unit &u, const KeyRange<kKeys> &kr, int S)
+__device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, int S, uint32_t &item, uint32_t &units)
 {
     const AttnParams &p = args.p;
+    const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
     const PagedCache &c = p.c;
     const int tid = threadIdx.x - kSoftmax, w = tid >> 5, lane = tid & 31, r8 = lane & 7, q4 = lane >> 3;
     const int n = u.tb - u.ta;
@@ -272,6 +345,23 @@ __device__ void load_tiles(Smem<D> &sm, const Args &args, const Unit &u, const K
         return __ldg(c.table + (size_t)u.row * c.width + (k0 >> c.ps_log2));
     };
     int pages = pages_of(0), pages_next = pages_of(1);
+    // queries: 16 (or 8) lanes for a row; rows past the unit's are zeros
+    if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
+    {
+        constexpr int LPR = D / 8;
+        const int g = tid % LPR;
+        for (int r = tid / LPR; r < u.halves * kHalf; r += kLoaders / LPR) {
+            const int t = (u.r0 + r) / p.G, hq = u.h * p.G + (u.r0 + r) - t * p.G;
+            const bool live = r < u.rows;
+            cp_async16(sm.q[0] + (r >> 7) * (kHalf * D * 2) + chunk_at(r & 127, g),
+                       live ? p.q + (u.c0 + t) * p.ql.token + hq * p.ql.head + g * 8 : p.q, live ? 16 : 0);
+        }
+    }
+    auto queries_done = [&]() {
+        cp_async_wait_all();
+        tc::fence_smem_to_async();
+        mbar_arrive(&sm.q_full);
+    };
     // source of this lane's key of group gi of tile i; null where nothing is read
     auto source = [&](const uint8_t *base, int i, int gi, int pg) -> const uint8_t * {
         const int k0 = kr.tile(u.ta + i) * kKeys + gi * 8, j = k0 + r8;
@@ -284,12 +374,13 @@ __device__ void load_tiles(Smem<D> &sm, const Args &args, const Unit &u, const K
     };
     if constexpr (!FP8) {
         for (int it = 0; it < 2 * n; it++) {
-            const int i = it >> 1, slot = it % kSlots, k0 = kr.tile(u.ta + i) * kKeys;
+            const uint32_t ring = item + it;
+            const int i = it >> 1, slot = ring % kSlots, k0 = kr.tile(u.ta + i) * kKeys;
             const uint8_t *base = it & 1 ? c.v : c.k;
             // every key is seen by some token and has a page (the four warps hold the same page ids)
             const bool whole = k0 + kKeys <= kr.end && (k0 >= kr.lo || k0 + kKeys <= S) &&
                                __all_sync(~0u, lane >= kKeys / 8 || (unsigned)pages < (unsigned)c.pages);
-            if (it >= kSlots && !wait_warp(sm, &sm.empty[slot], (it / kSlots - 1) & 1, c.err)) break;
+            if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
             if (whole) {
                 if (w == 0) {
                     if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kKeys * RB);
@@ -317,12 +408,14 @@ __device__ void load_tiles(Smem<D> &sm, const Args &args, const Unit &u, const K
                 tc::fence_smem_to_async();
                 mbar_arrive(&sm.full[slot]);
             }
+            if (it == 1) queries_done();   // the first keys and values were on their way meanwhile
             if (it & 1) {
                 pages = pages_next;
                 pages_next = pages_of(i + 2);
             }
         }
     } else {
+        queries_done();
         // codes pass through registers: the next item's loads are in flight while this one's are
         // converted (exactly) to the query's type and stored
         uint4 cur[GR * PASS > 0 ? GR * PASS : 1], nxt[GR * PASS > 0 ? GR * PASS : 1];
@@ -339,7 +432,8 @@ __device__ void load_tiles(Smem<D> &sm, const Args &args, const Unit &u, const K
         };
         fetch(0, cur, pages);
         for (int it = 0; it < 2 * n; it++) {
-            const int slot = it % kSlots;
+            const uint32_t ring = item + it;
+            const int slot = ring % kSlots;
             if (it + 1 < 2 * n) {
                 if (it & 1) {
                     pages = pages_next;
@@ -347,7 +441,7 @@ __device__ void load_tiles(Smem<D> &sm, const Args &args, const Unit &u, const K
                 }
                 fetch(it + 1, nxt, pages);
             }
-            if (it >= kSlots && !wait_warp(sm, &sm.empty[slot], (it / kSlots - 1) & 1, c.err)) break;
+            if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
 #pragma unroll
             for (int a = 0; a < GR; a++)
 #pragma unroll
@@ -365,6 +459,24 @@ __device__ void load_tiles(Smem<D> &sm, const Args &args, const Unit &u, const K
             for (int a = 0; a < GR * PASS; a++) cur[a] = nxt[a];
         }
     }
+    item += 2 * n;
+    units++;
+    return true;
+}
+
+template <int D, typename Q, bool FP8>
+__device__ void load_role(Smem<D> &sm, const Args &args, int W, int S)
+{
+    uint32_t item = 0, units = 0;
+    for (int k = 0; const Unit *at = unit_of(sm, k, args.p.c.err); k++) {
+        const Unit u = *at;
+        unit_done(sm, k);
+        if (u.tb > u.ta && !load_unit<D, Q, FP8>(sm, args, u, W, S, item, units)) break;
+    }
+    // where a wait gave up, tiles may still be landing: let them (the last one of each slot)
+    if (sm.stop)
+        for (uint32_t i = item < kSlots ? 0 : item - kSlots; i < item + kSlots; i++)
+            mbar_wait_bounded(&sm.full[i % kSlots], (i / kSlots) & 1, kLimitNs / 8);
 }
 
 struct SplitWs {   // partial results of split units: (m, l) and O by column, so that threads (rows) are contiguous
@@ -384,27 +496,42 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Unit &u, in
                             Q::pack(o[8 * i + 4] * f, o[8 * i + 5] * f), Q::pack(o[8 * i + 6] * f, o[8 * i + 7] * f));
 }
 
-// ---- warps 0-7: one thread per row
+// One row of a split unit from its pieces; `at`: the first piece's m of this row
 template <int D, typename Q, bool FP8>
-__device__ void softmax_rows(Smem<D> &sm, const AttnParams &p, const Unit &u, const KeyRange<kKeys> &kr, uint32_t tmem, int W, int S,
-                             float *partial)
+__device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const float *at)
+{
+    const int r = u.r0 + threadIdx.x;
+    constexpr size_t step = SplitWs::slot_floats(D);
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < u.pieces; i++) m = fmaxf(m, __ldcg(at + i * step));
+    const float base = m == -INFINITY ? 0.f : m;
+    for (int i = 0; i < u.pieces; i++) l += ex2(__ldcg(at + i * step) - base) * __ldcg(at + i * step + kRowsCta);
+    const float f = l == 0.f ? 0.f : (FP8 ? p.c.v_scale[p.layer * p.c.Hkv + u.h] : 1.f) / l;
+    for (int d = 0; d < D; d += 32) {
+        float o[32];
+#pragma unroll
+        for (int j = 0; j < 32; j++) o[j] = 0.f;
+        for (int i = 0; i < u.pieces; i++) {
+            const float a = ex2(__ldcg(at + i * step) - base);
+#pragma unroll
+            for (int j = 0; j < 32; j++) o[j] += a * __ldcg(at + i * step + (size_t)(2 + d + j) * kRowsCta);
+        }
+        store_row<Q>(p, u, r, d, o, f);
+    }
+    if (p.lse) p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far)
+template <int D, typename Q, bool FP8>
+__device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
+                             uint32_t &tiles, uint32_t &units)
 {
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, h = tid >> 7, rl = tid & 127, w = tid >> 5;
     const int n = u.tb - u.ta;
+    const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
     const int r = u.r0 + h * kHalf + rl;                         // row of the sequence
     const bool live = h * kHalf + rl < u.rows;
-    // this row's queries into shared memory
-    if (h < u.halves) {
-        const uint16_t *src = p.q + (long long)(u.c0 + r / p.G) * p.ql.token + (long long)(u.h * p.G + r % p.G) * p.ql.head;
-#pragma unroll
-        for (int g = 0; g < D / 8; g++)
-            *reinterpret_cast<uint4 *>(sm.q[h] + chunk_at(rl, g)) = live ? __ldg(reinterpret_cast<const uint4 *>(src) + g) : make_uint4(0, 0, 0, 0);
-        tc::fence_smem_to_async();
-    }
-    mbar_arrive(&sm.q_full);
-    if (h >= u.halves) return;
-    // (a scale of 0 as the least that keeps hidden scores at -inf)
     const float sc = fmaxf(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f), 1e-37f);
     const int first = u.len - u.n;
     const int pos = first + min(r, u.n * p.G - 1) / p.G;          // this row's position
@@ -415,11 +542,10 @@ __device__ void softmax_rows(Smem<D> &sm, const AttnParams &p, const Unit &u, co
     const uint32_t lane_base = tmem + ((uint32_t)(w & 3) * 32u << 16);
     const uint32_t ts = lane_base + Cols<D>::s(h), tp = lane_base + Cols<D>::p(h), to = lane_base + Cols<D>::o(h);
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
     for (int i = 0; i < n; i++) {
         const int k0 = kr.tile(u.ta + i) * kKeys;
         const bool all = k0 + kKeys - 1 <= p_lo && (k0 >= lo_all || k0 + kKeys <= S);
-        if (!(ok = wait_warp(sm, &sm.s_full[h], i & 1, c.err))) break;
+        if (!wait_warp(sm, &sm.s_full[h], (tiles + i) & 1, c.err)) return false;
         tc::fence_after_sync();
         uint32_t v[kKeys];
 #pragma unroll
@@ -432,13 +558,14 @@ __device__ void softmax_rows(Smem<D> &sm, const AttnParams &p, const Unit &u, co
             for (int j = 0; j < kKeys; j++)
                 if (!(j <= hi_j && (j >= lo_j || j < s_j))) v[j] = 0xff800000u;   // -inf
         }
-        float mx0 = __uint_as_float(v[0]), mx1 = __uint_as_float(v[1]);
+        float mx8[8];
 #pragma unroll
-        for (int j = 2; j < kKeys - 2; j += 4) {
-            mx0 = fmaxf(mx0, fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
-            mx1 = fmaxf(mx1, fmaxf(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])));
-        }
-        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(__uint_as_float(v[kKeys - 2]), __uint_as_float(v[kKeys - 1])));
+        for (int j = 0; j < 8; j++) mx8[j] = fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 8]));
+#pragma unroll
+        for (int j = 16; j < kKeys; j += 16)
+#pragma unroll
+            for (int x = 0; x < 8; x++) mx8[x] = fmaxf(fmaxf(mx8[x], __uint_as_float(v[j + x])), __uint_as_float(v[j + 8 + x]));
+        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])), fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
         const float m_new = fmaxf(m, mx * sc);
         if (i == 0) m = m_new;
         else if (__any_sync(~0u, m_new > m + kGrow)) {
@@ -456,28 +583,30 @@ __device__ void softmax_rows(Smem<D> &sm, const AttnParams &p, const Unit &u, co
             }
         }
         const float base = m == -INFINITY ? 0.f : m;
-        float s0 = 0.f, s1 = 0.f;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
         for (int q = 0; q < 2; q++) {
 #pragma unroll
-            for (int j = 64 * q; j < 64 * q + 64; j += 2) {
+            for (int j = 32 * q; j < 32 * q + 32; j++) {
                 float e0, e1;
-                tc::fma2(e0, e1, __uint_as_float(v[j]), __uint_as_float(v[j + 1]), sc, sc, -base, -base);
-                e0 = ex2(e0);
-                e1 = ex2(e1);
-                add2(s0, s1, e0, e1);
-                v[j / 2] = Q::pack(e0, e1);   // rounded to 16 bits for the product; l sums it unrounded
+                tc::fma2(e0, e1, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), sc, sc, -base, -base);
+                e0 = ex2(e0), e1 = ex2(e1);
+                if (j & 1) add2(s2, s3, e0, e1);
+                else add2(s0, s1, e0, e1);
+                v[j] = Q::pack(e0, e1);   // rounded to 16 bits for the product; l sums it unrounded
             }
             tmem_st32(tp + 32 * q, v + 32 * q);
         }
-        l += s0 + s1;
+        l += (s0 + s2) + (s1 + s3);
         tmem_wait_st();
         tc::fence_before_sync();
-        mbar_arrive(&sm.p_full[h]);
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&sm.p_full[h]);
     }
-    if (ok) ok = wait_warp(sm, &sm.o_full[h], 0, c.err);
+    if (!wait_warp(sm, &sm.o_full[h], units & 1, c.err)) return false;
     tc::fence_after_sync();
-    if (!ok) return;
+    tiles += n;
+    units++;
     const float f = l == 0.f ? 0.f : (FP8 ? c.v_scale[p.layer * c.Hkv + u.h] : 1.f) / l;
 #pragma unroll 1
     for (int q = 0; q < D / 32; q++) {
@@ -496,6 +625,167 @@ __device__ void softmax_rows(Smem<D> &sm, const AttnParams &p, const Unit &u, co
     } else if (live && p.lse) {
         p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+    return true;
+}
+
+// Meeting point of the eight softmax warps, bounded like every wait.
+template <int D>
+__device__ __forceinline__ bool softmax_sync(Smem<D> &sm, uint32_t &joins, int *err)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.join);
+    return wait_warp(sm, &sm.join, joins++ & 1, err);
+}
+
+template <int D, typename Q, bool FP8>
+__device__ void softmax_role(Smem<D> &sm, const AttnParams &p, uint32_t tmem, int W, int S)
+{
+    const int tid = threadIdx.x, h = tid >> 7;
+    int *count = reinterpret_cast<int *>(p.ws);
+    SplitWs ws;
+    ws.data = reinterpret_cast<float *>(p.ws + kAttnCounters * sizeof(int));
+    uint32_t tiles = 0, units = 0, joins = 0;
+    for (int k = 0; const Unit *at = unit_of(sm, k, p.c.err); k++) {
+        const Unit &u = *at;
+        float *partial = u.pieces > 1 ? ws.slot(u.idx, D) : nullptr;
+        if (u.tb == u.ta) {   // no token of the row tile sees a key
+            if (tid < u.rows) {
+                const float z[32] = {};
+                const int r = u.r0 + tid;
+                for (int d = 0; d < D; d += 32) store_row<Q>(p, u, r, d, z, 0.f);
+                if (p.lse) p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = -INFINITY;
+            }
+        } else {
+            if (h < u.halves && !softmax_unit<D, Q, FP8>(sm, p, u, tmem, W, S, partial, tiles, units)) return;
+            if (partial) {
+                // the last of a unit's CTAs joins the pieces, in their order
+                const int splits = p.splits, first = u.idx / splits;
+                __threadfence();
+                if (!softmax_sync(sm, joins, p.c.err)) return;
+                if (tid == 0) {
+                    const int done = atomicAdd(count + first, 1);
+                    sm.last = done == u.pieces - 1;
+                    if (sm.last) count[first] = 0;   // ready for the next call
+                    __threadfence();
+                }
+                if (!softmax_sync(sm, joins, p.c.err)) return;
+                if (sm.last && tid < u.rows) join_row<D, Q, FP8>(p, u, ws.slot(first * splits, D) + tid);
+                if (!softmax_sync(sm, joins, p.c.err)) return;   // sm.last is read
+            }
+        }
+        unit_done(sm, k);
+    }
+}
+
+// New tokens of sequence b and its row, 0 tokens where its offsets or its row do not fit (`report`: says so).
+__device__ __forceinline__ SeqInfo prefill_seq(const AttnParams &p, int b, int &c0, bool report)
+{
+    SeqInfo s;
+    s.row = s.len = s.n = 0;
+    s.ok = false;
+    c0 = p.cu[b];
+    const int c1 = p.cu[b + 1], row = p.rows[b];
+    if (c0 < 0 || c1 < c0 || c1 > p.total || c1 - c0 > p.T || (b > 0 && p.cu[b - 1] > c0)) {
+        if (report) atomicOr(p.c.err, KDA_DEVERR_SEQLEN);
+    } else if (c1 > c0) {
+        s = seq_info(p.c, row, c1 - c0, 0x7fffffff, report);
+        if (!s.ok) s.n = 0;
+    }
+    return s;
+}
+
+// ---- warp 13: units in order of their number, handed to the other roles a few ahead
+template <int D>
+__device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
+{
+    const PagedCache &c = p.c;
+    const int lane = threadIdx.x & 31, splits = p.splits;
+    int *counter = reinterpret_cast<int *>(p.ws) + kMaxSplitCtas;   // next unit, CTAs that are done
+    const int kept = min(p.B, kTable);
+    int all = sm.before[kept];
+    for (int b0 = kept; b0 < p.B; b0 += 32) {   // sequences past the table
+        int c0, t = 0;
+        if (b0 + lane < p.B) t = (prefill_seq(p, b0 + lane, c0, blockIdx.x == 0).n * p.G + kRowsCta - 1) / kRowsCta;
+        all += __reduce_add_sync(~0u, t);
+    }
+    const long long total = (long long)all * c.Hkv * splits;
+    long long idx = blockIdx.x;
+    for (int k = 0;; k++) {
+        const int slot = k % kUnits;
+        Unit u;
+        u.idx = -1;
+        if (idx < total) {
+            const int y = (int)(idx % splits), x = (int)(idx / splits) / c.Hkv;
+            const int want = all - 1 - x;   // the last row tiles first: the longest of a causal prompt
+            int b = -1, tile = 0;
+            if (want < sm.before[kept]) {
+                int a = 0, e = kept;        // the last sequence with before[] <= want, 32 at a time
+                while (e - a > 1) {
+                    const int step = (e - a + 31) / 32, at = a + lane * step;
+                    const unsigned m = __ballot_sync(~0u, at < e && sm.before[at] <= want);
+                    a += (31 - __clz(m)) * step;
+                    e = min(e, a + step);
+                }
+                b = a;
+                tile = want - sm.before[a];
+            } else {
+                int at = sm.before[kept];
+                for (int b0 = kept; b0 < p.B && b < 0; b0 += 32) {
+                    int c0, t = 0;
+                    if (b0 + lane < p.B) t = (prefill_seq(p, b0 + lane, c0, false).n * p.G + kRowsCta - 1) / kRowsCta;
+                    int inc = t;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int v = __shfl_up_sync(~0u, inc, o);
+                        if (lane >= o) inc += v;
+                    }
+                    const unsigned m = __ballot_sync(~0u, want < at + inc);
+                    if (m) {
+                        const int src = __ffs(m) - 1;
+                        b = b0 + src;
+                        tile = want - at - __shfl_sync(~0u, inc - t, src);
+                    }
+                    at += __shfl_sync(~0u, inc, 31);
+                }
+            }
+            const SeqInfo s = prefill_seq(p, b, u.c0, false);
+            u.idx = (int)idx;
+            u.h = (int)(idx / splits) % c.Hkv;
+            u.row = s.row;
+            u.n = s.n;
+            u.len = s.len;
+            u.r0 = tile * kRowsCta;
+            u.rows = min(kRowsCta, u.n * p.G - u.r0);
+            u.halves = u.rows > kHalf ? 2 : 1;
+            u.p_first = u.len - u.n + u.r0 / p.G;
+            u.p_last = u.len - u.n + (u.r0 + u.rows - 1) / p.G;
+            const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
+            // this split's share of the key tiles, two at least; splits past the last piece have none
+            const int share = max(2, (kr.count + splits - 1) / splits);
+            u.pieces = max(1, (kr.count + share - 1) / share);
+            u.ta = min(kr.count, y * share);
+            u.tb = min(kr.count, u.ta + share);
+            if (y >= u.pieces) {   // nothing to do: take another
+                int nxt = 0;
+                if (lane == 0) nxt = atomicAdd(counter, 1);
+                idx = (long long)gridDim.x + __shfl_sync(~0u, nxt, 0);
+                k--;
+                continue;
+            }
+        }
+        if (k >= kUnits && !wait_warp(sm, &sm.u_empty[slot], (k / kUnits - 1) & 1, c.err)) break;
+        if (lane == 0) {
+            sm.unit[slot] = u;
+            mbar_arrive(&sm.u_full[slot]);
+        }
+        __syncwarp();
+        if (u.idx < 0) break;
+        int nxt = 0;
+        if (lane == 0) nxt = atomicAdd(counter, 1);
+        idx = (long long)gridDim.x + __shfl_sync(~0u, nxt, 0);
+    }
+    // every CTA has taken its last number: the last one to say so leaves the counters ready for the next call
+    if (lane == 0 && atomicAdd(counter + 1, 1) == (int)gridDim.x - 1) counter[0] = counter[1] = 0;
 }
 
 template <int D, typename Q, bool FP8>
@@ -505,172 +795,90 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
     // the swizzle repeats every 1024 bytes of the shared address
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const AttnParams &p = args.p;
-    const PagedCache &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
-    const int splits = gridDim.y;
     if (tid == 0) {
-        mbar_init(&sm.q_full, kSoftmax);
+        mbar_init(&sm.q_full, kLoaders);
+        mbar_init(&sm.q_empty, 1);
+        mbar_init(&sm.join, kSoftmax / 32);
         mbar_init(&sm.drain, 1);
-        for (int i = 0; i < kSlots; i++) {
+        for (int i = 0; i < (int)kSlots; i++) {
             mbar_init(&sm.full[i], kLoaders);
             mbar_init(&sm.empty[i], 1);
         }
         for (int h = 0; h < 2; h++) {
             mbar_init(&sm.s_full[h], 1);
-            mbar_init(&sm.p_full[h], kHalf);
+            mbar_init(&sm.p_full[h], kHalf / 32);
             mbar_init(&sm.o_full[h], 1);
         }
+        for (int i = 0; i < kUnits; i++) {
+            mbar_init(&sm.u_full[i], 1);
+            mbar_init(&sm.u_empty[i], 13);   // the warps of the other roles
+        }
         sm.stop = 0;
-        sm.unit_b = -1;
         fence_mbar_init();
     }
-    __syncthreads();
     grid_dependency_wait();
+    // after the wait: a kernel that this one waits for may still need the SM's tensor memory
+    if (warp == 12) tc::tmem_alloc(&sm.tmem, 512);
 
-    // ---- which sequence and row tile: the CTAs count the tiles from the last one back, so that the
-    // longest ones of a causal prompt start first
-    if (warp == 0) {
-        const int x = blockIdx.x / c.Hkv;
-        const bool report = blockIdx.x == 0 && blockIdx.y == 0;
-        int before = 0, all = 0;
-        for (int pass = 0; pass < 2; pass++) {   // first the number of tiles, then the tile (in one go up to 32 sequences)
-            int want = all - 1 - x;
-            if (pass == 1 && want < 0) break;
-            before = 0;
-            for (int b0 = 0; b0 < p.B; b0 += 32) {
-                const int b = b0 + lane;
-                int tiles = 0, c0 = 0, n = 0;
-                if (b < p.B) {
-                    c0 = p.cu[b];
-                    const int c1 = p.cu[b + 1], row = p.rows[b];
-                    if (c0 < 0 || c1 < c0 || c1 > p.total || c1 - c0 > p.T || (b > 0 && p.cu[b - 1] > c0)) {
-                        if (report && pass == 0) atomicOr(c.err, KDA_DEVERR_SEQLEN);
-                    } else if (c1 > c0 && seq_info(c, row, c1 - c0, 0x7fffffff, report && pass == 0).ok) n = c1 - c0;
-                    tiles = (n * p.G + kRowsCta - 1) / kRowsCta;
-                }
-                int inc = tiles;
+    // ---- row tiles before each sequence, for the first kTable of them
+    {
+        static_assert(kTable == 2 * kThreads, "two sequences a thread");
+        const int kept = min(p.B, kTable), b = 2 * tid;
+        int c0, t0 = 0, t1 = 0;
+        if (b < kept) t0 = (prefill_seq(p, b, c0, blockIdx.x == 0).n * p.G + kRowsCta - 1) / kRowsCta;
+        if (b + 1 < kept) t1 = (prefill_seq(p, b + 1, c0, blockIdx.x == 0).n * p.G + kRowsCta - 1) / kRowsCta;
+        int inc = t0 + t1;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(~0u, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const int sum = __shfl_sync(~0u, inc, 31);
-                if (p.B <= 32) want = sum - 1 - x;
-                if ((pass == 1 || p.B <= 32) && want >= before + inc - tiles && want < before + inc) {
-                    sm.unit_b = b;
-                    sm.unit_tile = want - (before + inc - tiles);
-                    sm.c0 = c0;
-                    sm.n = n;
-                }
-                before += sum;
-            }
-            all = before;
-            if (p.B <= 32) break;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += y;
         }
-    }
-    __syncthreads();
-    Unit u;
-    u.b = sm.unit_b;
-    if (u.b < 0) return;
-    u.h = blockIdx.x % c.Hkv;
-    u.c0 = sm.c0;
-    u.n = sm.n;
-    u.row = p.rows[u.b];
-    u.len = c.lens[u.row];
-    u.r0 = sm.unit_tile * kRowsCta;
-    u.rows = min(kRowsCta, u.n * p.G - u.r0);
-    u.halves = u.rows > kHalf ? 2 : 1;
-    const int first = u.len - u.n;
-    const KeyRange<kKeys> kr(first + u.r0 / p.G, first + (u.r0 + u.rows - 1) / p.G, u.len, W, S);
-    // this CTA's share of the key tiles, two at least (a unit without keys has one CTA and no tile)
-    const int share = max(2, (kr.count + splits - 1) / splits), pieces = max(1, (kr.count + share - 1) / share);
-    if ((int)blockIdx.y >= pieces) return;
-    u.ta = blockIdx.y * share;
-    u.tb = min(kr.count, u.ta + share);
-    int *count = reinterpret_cast<int *>(p.ws) + blockIdx.x;
-    SplitWs ws;
-    ws.data = reinterpret_cast<float *>(p.ws + kMaxSplitCtas * sizeof(int));
-    float *partial = pieces > 1 ? ws.slot(blockIdx.x * splits + blockIdx.y, D) : nullptr;
-
-    if (kr.count == 0) {   // no token of the tile sees a key
-        for (int x = tid; x < u.rows * (D / 32); x += kThreads) {
-            const float z[32] = {};
-            const int r = u.r0 + x / (D / 32);
-            store_row<Q>(p, u, r, x % (D / 32) * 32, z, 0.f);
-            if (p.lse && x % (D / 32) == 0) p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = -INFINITY;
-        }
-        return;
-    }
-
-    if (warp == 12) {
-        tc::tmem_alloc(&sm.tmem, 512);
+        if (lane == 31) sm.warp_sum[warp] = inc;
         tc::fence_before_sync();
+        __syncthreads();
+        tc::fence_after_sync();
+        int off = inc - t0 - t1;
+        for (int i = 0; i < warp; i++) off += sm.warp_sum[i];
+        if (b <= kept) sm.before[b] = off;
+        if (b + 1 <= kept) sm.before[b + 1] = off + t0;
+        if (tid == kThreads - 1 && kept == kTable) sm.before[kTable] = off + t0 + t1;
+        tc::fence_before_sync();
+        __syncthreads();
+        tc::fence_after_sync();
     }
-    __syncthreads();
-    tc::fence_after_sync();
     const uint32_t tmem = sm.tmem;
     if (warp < 8) {
         regs_inc<kRegsSoftmax>();
-        softmax_rows<D, Q, FP8>(sm, p, u, kr, tmem, W, S, partial);
+        softmax_role<D, Q, FP8>(sm, p, tmem, W, S);
         __syncwarp();
         regs_dec<kRegs>();   // back to what the common code was compiled for
     } else if (warp < 12) {
         regs_dec<kRegsLoad>();
-        load_tiles<D, Q, FP8>(sm, args, u, kr, S);
+        load_role<D, Q, FP8>(sm, args, W, S);
         __syncwarp();
         regs_inc<kRegs>();
     } else {
         regs_dec<kRegsMma>();
-        if (warp == 12 && lane == 0) issue_products<D, Q>(sm, u, tmem, c.err);
+        if (warp == 12) mma_role<D, Q>(sm, __reduce_max_sync(~0u, tmem), p.c.err);
+        else if (warp == 13) unit_role<D>(sm, p, W, S);
         __syncwarp();
         regs_inc<kRegs>();
     }
     tc::fence_before_sync();
-    if (partial) __threadfence();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 12) {
-        if (sm.stop) {   // a wait gave up: let what was issued finish before the memory goes back
-            if (lane == 0) {
-                tc::commit(&sm.drain);
-                mbar_wait_bounded(&sm.drain, 0, kLimitNs);
-            }
-            __syncwarp();
-            tc::fence_after_sync();
+    if (sm.stop) {   // a wait gave up: let what was issued finish before the memory goes back
+        if (warp == 12) {
+            if (elect_one()) tc::commit(&sm.drain);
+            mbar_wait_bounded(&sm.drain, 0, kLimitNs);
         }
-        tc::tmem_dealloc(tmem, 512);
+        tc::fence_before_sync();
+        __syncthreads();
+        tc::fence_after_sync();
     }
-    if (!partial) return;
-    // ---- the last of a unit's CTAs joins the pieces, in their order
-    if (tid == 0) {
-        const int done = atomicAdd(count, 1);
-        sm.last = done == pieces - 1;
-        if (sm.last) *count = 0;   // ready for the next call
-        __threadfence();
-    }
-    __syncthreads();
-    if (!sm.last || tid >= u.rows) return;
-    const int r = u.r0 + tid;
-    const float *at = ws.slot(blockIdx.x * splits, D) + tid;
-    constexpr size_t step = SplitWs::slot_floats(D);
-    float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < pieces; i++) m = fmaxf(m, __ldcg(at + i * step));
-    const float base = m == -INFINITY ? 0.f : m;
-    for (int i = 0; i < pieces; i++) l += ex2(__ldcg(at + i * step) - base) * __ldcg(at + i * step + kRowsCta);
-    const float f = l == 0.f ? 0.f : (FP8 ? c.v_scale[p.layer * c.Hkv + u.h] : 1.f) / l;
-    for (int d = 0; d < D; d += 32) {
-        float o[32];
-#pragma unroll
-        for (int j = 0; j < 32; j++) o[j] = 0.f;
-        for (int i = 0; i < pieces; i++) {
-            const float a = ex2(__ldcg(at + i * step) - base);
-#pragma unroll
-            for (int j = 0; j < 32; j++) o[j] += a * __ldcg(at + i * step + (size_t)(2 + d + j) * kRowsCta);
-        }
-        store_row<Q>(p, u, r, d, o, f);
-    }
-    if (p.lse) p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (warp == 12) tc::tmem_dealloc(tmem, 512);
 }
 
 // The driver's tensor-map encoder, looked up once.
@@ -716,14 +924,16 @@ cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
     const long long by_total = (long long)p.total * p.G / kRowsCta + p.B;
     const long long by_len = (long long)p.B * (((long long)p.T * p.G + kRowsCta - 1) / kRowsCta);
     const long long tiles = by_total < by_len ? by_total : by_len, units = tiles * p.c.Hkv;
-    if (units > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    if (units > 0x7fffffffll) return cudaErrorInvalidValue;
     // too few units to fill the SMs: split the keys
     const int most = sms < kMaxSplitCtas ? sms : kMaxSplitCtas;
     const int splits = units * 2 <= most ? (int)(most / units) : 1;
     Args a = {};
     a.p = p;
     if (!FP8 && ((e = encode(&a.k, p.c.k, p.c)) != cudaSuccess || (e = encode(&a.v, p.c.v, p.c)) != cudaSuccess)) return e;
-    return launch_pdl(kda_attn_prefill_kernel<D, Q, FP8>, dim3((unsigned)units, (unsigned)splits), dim3(kThreads), smem, stream, a);
+    a.p.splits = splits;
+    const long long ctas = units * splits < sms ? units * splits : sms;
+    return launch_pdl(kda_attn_prefill_kernel<D, Q, FP8>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a);
 }
 
 template <int D>
@@ -735,7 +945,7 @@ cudaError_t launch_types(const AttnParams &p, cudaStream_t stream)
 
 }  // namespace
 
-size_t attn_prefill_workspace(int D) { return kMaxSplitCtas * sizeof(int) + kMaxSplitCtas * SplitWs::slot_floats(D) * sizeof(float); }
+size_t attn_prefill_workspace(int D) { return kAttnCounters * sizeof(int) + kMaxSplitCtas * SplitWs::slot_floats(D) * sizeof(float); }
 
 cudaError_t launch_attn_prefill(const AttnParams &p, cudaStream_t stream)
 {

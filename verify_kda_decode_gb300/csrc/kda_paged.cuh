@@ -61,6 +61,7 @@ struct AttnParams {
     const int *rows, *n_tokens, *cu;
     int B, T;                      // decode: tokens per sequence; prefill: bound on a sequence's tokens
     int total;                     // prefill: packed tokens
+    int splits;                    // prefill: CTAs that share a unit's keys (set by the launcher)
     const uint16_t *q;
     TokensLayout ql;
     uint16_t *out;
@@ -68,6 +69,9 @@ struct AttnParams {
     bool f16;
     uint8_t *ws;
 };
+// The attention workspace begins with counters (int, all 0 between calls), which both kernels use, then
+// holds partial results.
+constexpr size_t kAttnCounters = 4096;
 cudaError_t launch_attn_decode(const AttnParams &p, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const AttnParams &p, cudaStream_t stream);
 size_t attn_decode_workspace(int D);
