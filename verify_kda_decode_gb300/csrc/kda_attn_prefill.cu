@@ -48,7 +48,7 @@ constexpr uint32_t kSlots = 4;
 constexpr int kHalfBytes = kKeys * 128;   // a tile's 64 head dims: 128 rows of 128 bytes
 constexpr int kMaxSplitCtas = 256;             // CTAs of a launch whose keys are split
 constexpr uint64_t kLimitNs = 2000000000ull;   // bound of every wait
-constexpr int kUnits = 2, kTable = 1024;       // units on their way to the roles; sequences whose tile counts are kept on chip
+constexpr int kUnits = 2, kTable = 512;         // units on their way to the roles; sequences whose tile counts are kept on chip
 constexpr float kGrow = 8.f;                   // log2 growth of the maximum that O is rescaled for
 
 // What a CTA works on: rows [r0, r0 + rows) of the n * G of a sequence, and key tiles [ta, tb) of their range.
@@ -68,6 +68,7 @@ struct Smem {
     uint64_t q_full, q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
     Unit unit[kUnits];
     int before[kTable + 1], warp_sum[16];   // row tiles of the sequences before each one
+    int4 seq[kTable];                       // row, length, new tokens, first packed token
     uint32_t tmem;
     int last;
     volatile int stop;
@@ -346,17 +347,26 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
     };
     int pages = pages_of(0), pages_next = pages_of(1);
     // queries: 16 (or 8) lanes for a row; rows past the unit's are zeros
-    if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
-    {
-        constexpr int LPR = D / 8;
-        const int g = tid % LPR;
-        for (int r = tid / LPR; r < u.halves * kHalf; r += kLoaders / LPR) {
-            const int t = (u.r0 + r) / p.G, hq = u.h * p.G + (u.r0 + r) - t * p.G;
-            const bool live = r < u.rows;
-            cp_async16(sm.q[0] + (r >> 7) * (kHalf * D * 2) + chunk_at(r & 127, g),
-                       live ? p.q + (u.c0 + t) * p.ql.token + hq * p.ql.head + g * 8 : p.q, live ? 16 : 0);
+    auto load_queries = [&]() {
+        if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
+        constexpr int LPR = D / 8, STEP = kLoaders / LPR;   // lanes of a row, rows of a pass
+        const int g = tid % LPR, step_t = STEP / p.G, step_q = STEP - step_t * p.G;
+        int r = tid / LPR, t = (u.r0 + r) / p.G, q = u.r0 + r - t * p.G;   // the row's token and head of the group
+        const uint16_t *base = p.q + (long long)u.c0 * p.ql.token + (long long)(u.h * p.G) * p.ql.head + g * 8;
+#pragma unroll 2
+        for (int i = 0; i < 2 * kHalf / STEP; i++) {
+            if (r < u.halves * kHalf) {
+                const bool live = r < u.rows;
+                cp_async16(sm.q[0] + (r >> 7) * (kHalf * D * 2) + chunk_at(r & 127, g),
+                           live ? base + t * p.ql.token + q * p.ql.head : p.q, live ? 16 : 0);
+            }
+            r += STEP;
+            t += step_t;
+            q += step_q;
+            if (q >= p.G) q -= p.G, t++;
         }
-    }
+        return true;
+    };
     auto queries_done = [&]() {
         cp_async_wait_all();
         tc::fence_smem_to_async();
@@ -408,6 +418,7 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
                 tc::fence_smem_to_async();
                 mbar_arrive(&sm.full[slot]);
             }
+            if (it == 0 && !load_queries()) return false;
             if (it == 1) queries_done();   // the first keys and values were on their way meanwhile
             if (it & 1) {
                 pages = pages_next;
@@ -415,6 +426,7 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
             }
         }
     } else {
+        if (!load_queries()) return false;
         queries_done();
         // codes pass through registers: the next item's loads are in flight while this one's are
         // converted (exactly) to the query's type and stored
@@ -485,15 +497,26 @@ struct SplitWs {   // partial results of split units: (m, l) and O by column, so
     __device__ float *slot(int s, int D) const { return data + (size_t)s * slot_floats(D); }
 };
 
+// 32 outputs of a row.  A warp's rows are apart, so each store instruction goes to 32 lines: whole 32-byte
+// sectors where the output's alignment allows it, which halves their number.
 template <typename Q>
 __device__ __forceinline__ void store_row(const AttnParams &p, const Unit &u, int r, int d, const float *o, float f)
 {
-    const int tok = u.c0 + r / p.G, hq = u.h * p.G + r % p.G;
-    uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)tok * p.Hq + hq) * p.c.D + d);
+    const int t = r / p.G, tok = u.c0 + t, hq = u.h * p.G + r - t * p.G;
+    uint16_t *dst = p.out + ((size_t)tok * p.Hq + hq) * p.c.D + d;
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-        dst[i] = make_uint4(Q::pack(o[8 * i] * f, o[8 * i + 1] * f), Q::pack(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                            Q::pack(o[8 * i + 4] * f, o[8 * i + 5] * f), Q::pack(o[8 * i + 6] * f, o[8 * i + 7] * f));
+    for (int i = 0; i < 16; i++) w[i] = Q::pack(o[2 * i] * f, o[2 * i + 1] * f);
+    if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                         ::"l"(dst + 16 * i), "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]),
+                           "r"(w[8 * i + 4]), "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7]) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
 }
 
 // One row of a split unit from its pieces; `at`: the first piece's m of this row
@@ -748,7 +771,9 @@ __device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
                     at += __shfl_sync(~0u, inc, 31);
                 }
             }
-            const SeqInfo s = prefill_seq(p, b, u.c0, false);
+            SeqInfo s;
+            if (b < kept) s.row = sm.seq[b].x, s.len = sm.seq[b].y, s.n = sm.seq[b].z, u.c0 = sm.seq[b].w;
+            else s = prefill_seq(p, b, u.c0, false);
             u.idx = (int)idx;
             u.h = (int)(idx / splits) % c.Hkv;
             u.row = s.row;
@@ -824,12 +849,16 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
 
     // ---- row tiles before each sequence, for the first kTable of them
     {
-        static_assert(kTable == 2 * kThreads, "two sequences a thread");
-        const int kept = min(p.B, kTable), b = 2 * tid;
-        int c0, t0 = 0, t1 = 0;
-        if (b < kept) t0 = (prefill_seq(p, b, c0, blockIdx.x == 0).n * p.G + kRowsCta - 1) / kRowsCta;
-        if (b + 1 < kept) t1 = (prefill_seq(p, b + 1, c0, blockIdx.x == 0).n * p.G + kRowsCta - 1) / kRowsCta;
-        int inc = t0 + t1;
+        static_assert(kTable == kThreads, "one sequence a thread");
+        const int kept = min(p.B, kTable);
+        int tiles = 0;
+        if (tid < kept) {
+            int c0;
+            const SeqInfo q = prefill_seq(p, tid, c0, blockIdx.x == 0);
+            sm.seq[tid] = make_int4(q.row, q.len, q.n, c0);
+            tiles = (q.n * p.G + kRowsCta - 1) / kRowsCta;
+        }
+        int inc = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(~0u, inc, o);
@@ -839,11 +868,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
         tc::fence_before_sync();
         __syncthreads();
         tc::fence_after_sync();
-        int off = inc - t0 - t1;
+        int off = inc - tiles;
         for (int i = 0; i < warp; i++) off += sm.warp_sum[i];
-        if (b <= kept) sm.before[b] = off;
-        if (b + 1 <= kept) sm.before[b + 1] = off + t0;
-        if (tid == kThreads - 1 && kept == kTable) sm.before[kTable] = off + t0 + t1;
+        if (tid <= kept) sm.before[tid] = off;
+        if (tid == kThreads - 1 && kept == kTable) sm.before[kTable] = off + tiles;
         tc::fence_before_sync();
         __syncthreads();
         tc::fence_after_sync();
