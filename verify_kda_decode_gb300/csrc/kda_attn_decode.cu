@@ -107,6 +107,22 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Four E4M3 codes -> four halves in order; exact.
+__device__ __forceinline__ void e4m3x4_half4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const uint8_t *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const uint8_t *src, bool read)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
 // Runs of tiles are counted in 64 bits (rows that share pages can hold more keys than memory); the
 // divisions take the 32-bit path whenever the numbers allow it.
 __device__ __forceinline__ long long div_pos(long long a, long long b)
@@ -216,8 +232,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         const int p0 = seq.len - seq.n;
         const KeyRange<kTileKeys> kr(p0, seq.len - 1, seq.len, W, S);
         const int lo_all = (int)max(0ll, (long long)seq.len - W);         // every token sees [lo_all, p0]
-        const size_t head_bytes = (size_t)c.ps * C::RB;
-        const size_t layer_off = (size_t)p.layer * c.pages;
+        const uint32_t page_bytes = (uint32_t)c.page_bytes();   // under 2^27
+        const uint8_t *k_base = c.k + ((size_t)p.layer * c.pages * c.Hkv + h) * ((size_t)c.ps * C::RB) + lane * 16;
+        const ptrdiff_t v_minus_k = c.v - c.k;
+        // where a lane's pieces go: the swizzles of a step's rows differ from its first row's by constants
+        const uint32_t dst_k = (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_k(lane / C::CH)) * 16);
+        const uint32_t dst_v = (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_v(lane / C::CH)) * 16);
 
         // queries: rows nb * 8 + g, the elements this thread multiplies.  With an E4M3 cache the products are
         // taken in halves: a bfloat16 row is brought to a maximum in [1, 2) by a power of two first (exact
@@ -320,14 +340,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                     if (!ok) {
                         if (lane == 0) atomicOr(c.err, KDA_DEVERR_PAGE);
                     } else {
-                        const size_t off = ((layer_off + page) * c.Hkv + h) * head_bytes + (size_t)(k0 & (c.ps - 1)) * C::RB;
-                        uint8_t *dk = ring_p + stage * C::STAGE, *dv = dk + kStep * C::RB;
+                        // this lane's pieces: 16 bytes of row r0 + i * 32 / CH, all 512 bytes apart
+                        const uint8_t *sk = k_base + (size_t)(uint32_t)page * page_bytes + (k0 & (c.ps - 1)) * C::RB, *sv = sk + v_minus_k;
+                        const uint32_t dk = ring + stage * C::STAGE + dst_k, dv = ring + stage * C::STAGE + kStep * C::RB;
+                        constexpr int PER = 32 / C::CH;   // rows of a piece's step
+                        if (k0 + kStep <= kr.end && (k0 >= kr.lo || k0 + kStep <= S)) {
 #pragma unroll
-                        for (int i = 0; i < kStep * C::CH / 32; i++) {
-                            const int q = i * 32 + lane, r = q / C::CH, x = q % C::CH, j = k0 + r;
-                            const uint32_t n = j < kr.end && (j >= kr.lo || j < S) ? 16 : 0;
-                            cp_async16(dk + r * C::RB + ((x ^ C::swz_k(r)) * 16), c.k + off + (size_t)q * 16, n);
-                            cp_async16(dv + r * C::RB + ((x ^ C::swz_v(r)) * 16), c.v + off + (size_t)q * 16, n);
+                            for (int i = 0; i < kStep / PER; i++) {
+                                cp16(dk + i * 512, sk + i * 512);
+                                cp16(dv + i * 512 + (dst_v ^ (C::swz_v(i * PER) * 16)), sv + i * 512);
+                            }
+                        } else {   // zeros for the keys that no token sees
+#pragma unroll
+                            for (int i = 0; i < kStep / PER; i++) {
+                                const int j = k0 + i * PER + lane / C::CH;
+                                const bool read = j < kr.end && (j >= kr.lo || j < S);
+                                cp16_or_zero(dk + i * 512, sk + i * 512, read);
+                                cp16_or_zero(dv + i * 512 + (dst_v ^ (C::swz_v(i * PER) * 16)), sv + i * 512, read);
+                            }
                         }
                     }
                 }
@@ -369,7 +399,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                     if constexpr (FP8) {
 #pragma unroll
                         for (int u = 0; u < 4; u++) {
-                            const uint32_t a[4] = {e4m3x2_half2(xs[u], 0), e4m3x2_half2(ys[u], 0), e4m3x2_half2(xs[u], 1), e4m3x2_half2(ys[u], 1)};
+                            uint32_t a[4];
+                            e4m3x4_half4(xs[u], a[0], a[2]);
+                            e4m3x4_half4(ys[u], a[1], a[3]);
                             qk(4 * j + u, a);
                         }
                     } else {
@@ -382,44 +414,49 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                 }
                 // s[nb]: keys k0 + g (+ 8), rows nb * 8 + 2 cc (+ 1); in units of log2
                 const bool all = k0 + kStep - 1 <= p0 && (k0 >= lo_all || k0 + kStep <= S);
+                // The maximum is moved (by all of a row's lanes) only when a score passes it by more than 2^8: the
+                // usual step has no exchange between lanes.  P stays below 2^8, l and O have its scale.
+                bool grown = false;
 #pragma unroll
-                for (int nb = 0; nb < NB; nb++)
+                for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         s[nb][i] = (s[nb][i] + s2[nb][i]) * sc[nb][i & 1];
                         if (!all && !key_visible(k0 + g + 8 * (i >> 1), row_pos[nb][i & 1], W, S)) s[nb][i] = -INFINITY;
                     }
+#pragma unroll
+                    for (int i = 0; i < 2; i++) grown |= fmaxf(s[nb][i], s[nb][i + 2]) > row_m[nb][i] + 8.f;
+                }
+                if (__any_sync(~0u, grown)) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            float mx = fmaxf(s[nb][i], s[nb][i + 2]);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                            const float m_new = fmaxf(row_m[nb][i], mx);
+                            const float alpha = m_new == -INFINITY ? 1.f : ex2(row_m[nb][i] - m_new);
+                            row_m[nb][i] = m_new;
+                            row_l[nb][i] *= alpha;
+#pragma unroll
+                            for (int m = 0; m < MT; m++) acc[m][nb][i] *= alpha, acc[m][nb][2 + i] *= alpha;
+                        }
+                }
                 uint32_t pf[NB][2];
-                bool grown = false;
-                float alpha[NB][2];
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        float mx = fmaxf(s[nb][i], s[nb][i + 2]);
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-                        const float m_new = fmaxf(row_m[nb][i], mx);
-                        const float base = m_new == -INFINITY ? 0.f : m_new;   // a row that has seen no key yet
-                        grown |= m_new > row_m[nb][i];
-                        alpha[nb][i] = ex2(row_m[nb][i] - base);
-                        row_m[nb][i] = m_new;
+                        const float base = row_m[nb][i] == -INFINITY ? 0.f : row_m[nb][i];   // a row that has seen no key yet
                         s[nb][i] = ex2(s[nb][i] - base);
                         s[nb][i + 2] = ex2(s[nb][i + 2] - base);
-                        row_l[nb][i] = row_l[nb][i] * alpha[nb][i] + (s[nb][i] + s[nb][i + 2]);
+                        row_l[nb][i] += s[nb][i] + s[nb][i + 2];
                     }
                     // P is rounded to the product's 16-bit type (relative error 2^-9 or 2^-12, as the
                     // output's own rounding); l sums it unrounded
                     pf[nb][0] = transpose8x8(P::pack(s[nb][0], s[nb][1]));
                     pf[nb][1] = transpose8x8(P::pack(s[nb][2], s[nb][3]));
-                }
-                if (__any_sync(~0u, grown)) {
-#pragma unroll
-                    for (int m = 0; m < MT; m++)
-#pragma unroll
-                        for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-                            for (int i = 0; i < 4; i++) acc[m][nb][i] *= alpha[nb][i & 1];
                 }
                 const int kk[4] = {2 * cc, 2 * cc + 1, 2 * cc + 8, 2 * cc + 9};
                 auto pv = [&](int m, const uint32_t v0, const uint32_t v1, const uint32_t v2, const uint32_t v3) {
@@ -454,10 +491,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                         }
                     }
 #pragma unroll
-                    for (int u = 0; u < NW; u++)
+                    for (int u = 0; u < NW; u++) {
+                        // codes of two keys side by side before the conversion: (a0 b0 a1 b1), (a2 b2 a3 b3)
+                        uint32_t e[2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            e4m3x4_half4(__byte_perm(v[2 * i][u], v[2 * i + 1][u], 0x5140), e[0][2 * i], e[0][2 * i + 1]);
+                            e4m3x4_half4(__byte_perm(v[2 * i][u], v[2 * i + 1][u], 0x7362), e[1][2 * i], e[1][2 * i + 1]);
+                        }
 #pragma unroll
                         for (int hf = 0; hf < 2; hf++)
-                            pv(2 * u + hf, e4m3x2_half2(v[0][u], hf), e4m3x2_half2(v[1][u], hf), e4m3x2_half2(v[2][u], hf), e4m3x2_half2(v[3][u], hf));
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++) mma16816<P>(acc[2 * u + hf][nb], e[hf], pf[nb][0], pf[nb][1]);
+                    }
                 }
             }
             __syncwarp();   // the stage is read: the next issue may overwrite it
