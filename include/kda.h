@@ -307,7 +307,7 @@ typedef struct {
     int32_t num_layers, num_pages, num_kv_heads;
     int32_t page_size;       /* 16, 32, 64 or 128 */
     int32_t head_dim;        /* 64 or 128 */
-    int32_t rows, max_pages; /* page table: rows x max_pages */
+    int32_t rows, max_pages; /* page table: rows (at most 2^18) x max_pages */
     int32_t *page_table;     /* [rows, max_pages] */
     int32_t *seq_lens;       /* [rows] */
     int32_t *page_refs;      /* [num_pages] */
@@ -326,8 +326,8 @@ size_t kda_kv_workspace_size(const kda_kv_cache *cache);
  * too, the row gets a copy of it first (the copied page's id comes before those of the added
  * pages), in every layer.  A row for which not enough free pages are left (after those asked
  * for by all earlier rows of the call) or whose table is full sets KDA_DEVERR_NOPAGES and is
- * left as it was.  rows[i] must be distinct: a repeated row sets KDA_DEVERR_SLOT and only its
- * first entry counts; so does a row outside [0, cache->rows).  A negative count sets
+ * left as it was.  rows[i] must be distinct: a row that is named twice, or is outside
+ * [0, cache->rows), sets KDA_DEVERR_SLOT and none of its entries counts.  A negative count sets
  * KDA_DEVERR_TOKENS.  0 tokens leave a row as it is. */
 kda_status kda_kv_extend(const kda_kv_cache *cache, const int32_t *rows, const int32_t *n_tokens,
                          int32_t n_all, int32_t B, void *workspace, size_t workspace_bytes,
@@ -342,7 +342,7 @@ kda_status kda_kv_truncate(const kda_kv_cache *cache, const int32_t *rows, const
 /* Row dst_rows[i] gives its pages back and becomes a copy of row src_rows[i] that shares all of
  * its pages; no data moves until one of them extends past a shared, partly filled page.
  * A destination that is repeated, out of range or also a source of the call sets
- * KDA_DEVERR_SLOT and its entry is left out (a repeated one counts once). */
+ * KDA_DEVERR_SLOT and none of its entries counts. */
 kda_status kda_kv_fork(const kda_kv_cache *cache, const int32_t *src_rows, const int32_t *dst_rows,
                        int32_t n, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -29,7 +29,12 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kStep = 16;                 // keys of one warp step
 constexpr int kTileKeys = kWarps * kStep; // keys of one tile: 16 for each warp
 constexpr int kMaxCtas = 1024;            // bound of the grid, sizes the workspace
-constexpr int kMaxRows = 32;
+constexpr int kUnitRows = 32;
+// A unit counts for this many tiles more than it has: starting one (queries, page ids, the first keys,
+// the merge) takes as long as some tiles.  Without it a run of one-tile units held the call up: 64 ragged
+// sequences, four drafts, 1024 window: 70 us, with 2 / 4 / 8: 47 / 41 / 41 us; 131072 tokens of one
+// sequence: 91 us, 90 / 89 / 94 us.
+constexpr int kUnitCost = 4;
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
@@ -72,8 +77,8 @@ struct Cfg {
     static constexpr int CH = RB / 16;                    // its 16-byte chunks
     static constexpr int STAGE = 2 * kStep * RB;          // keys, then values
     // CTAs of an SM: as many as the accumulators (D NB / 4 registers) leave room for.  A warp's step is a
-    // chain of latencies (scores, maximum over lanes, exponentials, product), which other warps cover:
-    // with two CTAs everywhere an E4M3 cache (64 x 4096 tokens, 8 heads) took 153 us, OCC4_E4M3.
+    // chain of latencies (scores, exponentials, product), which other warps cover: two CTAs everywhere
+    // against this, 64 x 4096 tokens, 8 heads, E4M3: 153 us, 129 us; bfloat16 (HBM bound) 171 us both.
     static constexpr int OCC = D * NB >= 512 ? 2 : (RB == 256 || D * NB >= 256) ? 3 : 4;
     static constexpr bool Q_SMEM = NB > 1;                // queries in shared memory instead of registers
     static constexpr int Q_BYTES = Q_SMEM ? NB * 8 * D * 2 : 0;
@@ -96,7 +101,7 @@ struct Partials {   // workspace: counters, then for each CTA two slots of (m, l
     float *data;
     static constexpr size_t kCounters = kAttnCounters;
     static_assert(kCounters >= 3 * kMaxCtas, "units and groups");
-    static constexpr size_t slot_floats(int D) { return (size_t)kMaxRows * (D + 2); }
+    static constexpr size_t slot_floats(int D) { return (size_t)kUnitRows * (D + 2); }
     __device__ float *slot(int s, int D) const { return data + (size_t)s * slot_floats(D); }
 };
 
@@ -154,12 +159,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
     // ---- this CTA's run of tiles
     auto load_seq = [&](int b, bool report) { return seq_info(c, p.rows[b], p.n_tokens ? p.n_tokens[b] : p.T, p.T, report); };
     auto tiles_of = [&](const SeqInfo &s, int &kt, int &mt) -> long long {   // kt tiles in each of Hkv * mt units
+        // (the line of work gives each unit kUnitCost places, then one for each of its tiles)
         kt = mt = 0;
         if (!s.ok || s.n == 0) return 0;
         const KeyRange<kTileKeys> r(s.len - s.n, s.len - 1, s.len, W, S);
         kt = max(1, r.count);
         mt = (s.n * p.G + ROWS - 1) / ROWS;
-        return (long long)kt * mt * c.Hkv;
+        return (long long)(kt + kUnitCost) * mt * c.Hkv;
     };
     const int per = (p.B + kThreads - 1) / kThreads, b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
     long long mine = 0;
@@ -224,10 +230,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             seq = seq_of(++b);
             seq_tiles = tiles_of(seq, kt, mt);
         }
-        const int local = (int)div_pos(at - prefix, kt);
+        const int local = (int)div_pos(at - prefix, kt + kUnitCost);
         const int h = local / mt, mb = local % mt;
-        const long long u0 = prefix + (long long)local * kt;              // the unit's tiles [u0, u0 + kt)
-        const int ta = (int)(at - u0), tb = (int)min((long long)kt, end - u0);
+        const long long u0 = prefix + (long long)local * (kt + kUnitCost) + kUnitCost;   // the unit's tiles: places [u0, u0 + kt)
+        if (u0 >= end) break;   // they belong to the next CTAs
+        const int ta = (int)(max(at, u0) - u0), tb = (int)min((long long)kt, end - u0);
         const int n_rows = min(ROWS, seq.n * p.G - mb * ROWS);
         const int p0 = seq.len - seq.n;
         const KeyRange<kTileKeys> kr(p0, seq.len - 1, seq.len, W, S);
@@ -562,10 +569,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             }
             if (f == l) store(r, d, o, ls, m);
             else {
-                __stcg(reinterpret_cast<float4 *>(slot + 2 * kMaxRows + r * D + d), o);
+                __stcg(reinterpret_cast<float4 *>(slot + 2 * kUnitRows + r * D + d), o);
                 if (d == 0) {
                     __stcg(slot + r, m);
-                    __stcg(slot + kMaxRows + r, ls);
+                    __stcg(slot + kUnitRows + r, ls);
                 }
             }
         }
@@ -584,13 +591,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                     for (int i = i0; i < i1; i += step) {
                         const float *q = part.slot(2 * (f + i) + (i == 0), D);
                         const float a = ex2(__ldcg(q + r) - base);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(q + 2 * kMaxRows + r * D + d));
-                        ls += a * __ldcg(q + kMaxRows + r);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(q + 2 * kUnitRows + r * D + d));
+                        ls += a * __ldcg(q + kUnitRows + r);
                         o.x += a * y.x, o.y += a * y.y, o.z += a * y.z, o.w += a * y.w;
                     }
                     if (last) store(r, d, o, ls, m);
                     else {
-                        __stcg(reinterpret_cast<float4 *>(to + 2 * kMaxRows + r * D + d), o);
+                        __stcg(reinterpret_cast<float4 *>(to + 2 * kUnitRows + r * D + d), o);
                         // the row's (m, l) are still read by its other threads: kept apart until all are done
                         if (d == 0) mg_m[r] = m, mg_l[r] = ls;
                     }
@@ -599,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                     __syncthreads();
                     if (tid < n_rows) {
                         __stcg(to + tid, mg_m[tid]);
-                        __stcg(to + kMaxRows + tid, mg_l[tid]);
+                        __stcg(to + kUnitRows + tid, mg_l[tid]);
                     }
                 }
             };

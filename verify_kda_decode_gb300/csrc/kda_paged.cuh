@@ -9,6 +9,7 @@ namespace kda {
 
 constexpr int kMaxAttnT = 16;      // new tokens per sequence of a decode / verify call
 constexpr int kMaxGroup = 64;      // query heads per key head
+constexpr int kMaxRows = 1 << 18;  // rows of a page table
 
 struct PagedCache {
     uint8_t *k, *v;                // [layers, pages, Hkv, ps, D]
@@ -27,6 +28,7 @@ struct KvCall {
     PagedCache c;
     const int *rows, *arg;         // arg: n_tokens / new_lens / src_rows
     int uniform, B;
+    int lanes;                     // threads of an entry (set by the launcher)
     int *ws;                       // see kv_workspace_ints
     int *remap;
 };
@@ -36,8 +38,8 @@ constexpr int kKvMeta = 16, kKvRowArrays = 8;
 inline size_t kv_workspace_ints(int rows, int pages) { return kKvMeta + (size_t)kKvRowArrays * rows + 2 * (size_t)pages; }
 
 cudaError_t launch_kv_extend(const KvCall &p, cudaStream_t stream);
-cudaError_t launch_kv_truncate(const KvCall &p, cudaStream_t stream);
-cudaError_t launch_kv_fork(const KvCall &p, cudaStream_t stream);
+cudaError_t launch_kv_truncate(KvCall p, cudaStream_t stream);
+cudaError_t launch_kv_fork(KvCall p, cudaStream_t stream);
 cudaError_t launch_kv_compact(const KvCall &p, cudaStream_t stream);
 
 struct TokensLayout { long long seq, token, head; };   // strides in elements
@@ -97,11 +99,12 @@ inline cudaError_t paged_sm_count(int *sms)
 
 // launch_pdl with clusters of `cluster` CTAs.
 template <typename Kern, typename Arg>
-cudaError_t launch_pdl_cluster(Kern kern, dim3 grid, dim3 block, int cluster, cudaStream_t stream, const Arg &arg)
+cudaError_t launch_pdl_cluster(Kern kern, dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream, const Arg &arg)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -55,6 +55,7 @@ kda_status check_cache(const kda_kv_cache *cache)
         return fail(KDA_ERR_UNSUPPORTED, "page_size=%d: only 16, 32, 64 and 128 are built", cache->page_size);
     if (cache->head_dim != 64 && cache->head_dim != 128)
         return fail(KDA_ERR_UNSUPPORTED, "head_dim=%d: only 64 and 128 are built", cache->head_dim);
+    if (cache->rows > kda::kMaxRows) return fail(KDA_ERR_UNSUPPORTED, "rows=%d: at most %d", cache->rows, kda::kMaxRows);
     if ((long long)cache->rows * cache->max_pages > 0x7fffffffll)
         return fail(KDA_ERR_UNSUPPORTED, "rows * max_pages = %lld does not fit 31 bits", (long long)cache->rows * cache->max_pages);
     if ((long long)cache->max_pages * cache->page_size > 0x3fffffffll)
