@@ -212,31 +212,40 @@ __global__ void __launch_bounds__(kNt, 1) kda_kv_extend_kernel(const KvCall p)
     }
 }
 
-// Copies the filled tokens of the shared pages that extend replaced, in every layer: items
-// (copy, layer, k or v, head), one warp each, 16 bytes a lane.  Most calls have none, so the grid
-// is small and the count is read first.
+// Copies the filled tokens of the shared pages that extend replaced, in every layer: 2 KiB pieces of a
+// head's tokens, a warp each with four 16-byte loads a lane in flight (a warp for a head's whole run of
+// tokens took 20 us for 64 copies of up to 64 tokens, 4 heads, 4 layers; its loads waited for one another).
+// Most calls have none, and the count is read first.
+constexpr int kTail = 2048;
 __global__ void __launch_bounds__(256) kda_kv_copy_tails_kernel(const KvCall p)
 {
     const PagedCache &c = p.c;
     const Scratch s(p);
     grid_dependency_wait();
-    const int n = s.meta[0];
-    const long long items = (long long)n * c.layers * 2 * c.Hkv;
-    const int lane = threadIdx.x & 31;
+    const int n = s.meta[0], lane = threadIdx.x & 31;
     const size_t row = (size_t)c.D * c.elem(), head = row * c.ps;
+    const int pieces = (int)((head + kTail - 1) / kTail);
+    const long long items = (long long)n * c.layers * 2 * c.Hkv * pieces;
     for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (long long)gridDim.x * 8) {
         long long x = it;
+        const int piece = (int)(x % pieces);
+        x /= pieces;
         const int h = (int)(x % c.Hkv);
         x /= c.Hkv;
         const int kv = (int)(x & 1);
         x >>= 1;
         const int layer = (int)(x % c.layers), i = (int)(x / c.layers);
-        uint8_t *base = (kv ? c.v : c.k) + (size_t)layer * c.pages * c.page_bytes() + h * head;
+        const int chunks = (int)(s.cow_n[i] * row) / 16 - piece * (kTail / 16);   // left from this piece on
+        uint8_t *base = (kv ? c.v : c.k) + (size_t)layer * c.pages * c.page_bytes() + h * head + (size_t)piece * kTail;
         const uint4 *src = reinterpret_cast<const uint4 *>(base + (size_t)s.cow_src[i] * c.page_bytes());
         uint4 *dst = reinterpret_cast<uint4 *>(base + (size_t)s.cow_dst[i] * c.page_bytes());
-        const int chunks = (int)(s.cow_n[i] * row / 16);
-#pragma unroll 4
-        for (int q = lane; q < chunks; q += 32) __stcs(dst + q, __ldcs(src + q));
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            if (lane + 32 * u < chunks) v[u] = __ldcs(src + lane + 32 * u);
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            if (lane + 32 * u < chunks) __stcs(dst + lane + 32 * u, v[u]);
     }
 }
 
@@ -425,9 +434,8 @@ __global__ void __launch_bounds__(256) kda_kv_move_kernel(const KvCall p)
 // One warp per new token: lanes over the token's 16-byte source pieces (8 elements), keys then
 // values.  Pure data movement, bound by HBM for prompts and by the launch for a decode step.
 template <bool E4M3, bool F16>
-__device__ __forceinline__ void append_piece(const uint16_t *src, uint8_t *dst, float scale)
+__device__ __forceinline__ void append_piece(const uint4 w, uint8_t *dst, float scale)
 {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(src));
     if constexpr (!E4M3) {
         *reinterpret_cast<uint4 *>(dst) = w;
     } else {
@@ -478,8 +486,22 @@ __global__ void __launch_bounds__(256) kda_kv_append_kernel(const AppendParams p
     const long long tokens = p.cu ? p.T : (long long)p.B * p.T;
     grid_dependency_wait();
     if (tok >= tokens) return;
+    // The token's first pieces are on their way while its place is found, a chain of five loads (offsets, row,
+    // length, page) that took longer than moving the data.
+    const int per_log2 = c.D == 128 ? 4 : 3, pieces = c.Hkv << per_log2;   // 8 elements each
+    const long long seq = p.cu ? 0 : tok / p.T, in_seq = tok - seq * p.T;
+    const uint16_t *ks = p.k + (p.cu ? 0 : seq * p.kl.seq) + in_seq * p.kl.token, *vs = p.v + (p.cu ? 0 : seq * p.vl.seq) + in_seq * p.vl.token;
+    constexpr int kAhead = 4;
+    uint4 kw[kAhead], vw[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; a++) {
+        const int q = lane + 32 * a, h = q >> per_log2, i = q & ((1 << per_log2) - 1);
+        if (q < pieces) {
+            kw[a] = __ldcs(reinterpret_cast<const uint4 *>(ks + h * p.kl.head + i * 8));
+            vw[a] = __ldcs(reinterpret_cast<const uint4 *>(vs + h * p.vl.head + i * 8));
+        }
+    }
     int b, t, n;
-    long long koff, voff;
     if (p.cu) {
         // the sequence whose offsets hold this row: the last b with cu[b] <= tok, 32 at a time
         int a = 0, e = p.B;   // in [a, e)
@@ -501,14 +523,10 @@ __global__ void __launch_bounds__(256) kda_kv_append_kernel(const AppendParams p
         if (tok < c0 || tok >= c1) return;   // rows outside every sequence
         t = (int)(tok - c0);
         n = c1 - c0;
-        koff = tok * p.kl.token;
-        voff = tok * p.vl.token;
     } else {
-        b = (int)(tok / p.T);
-        t = (int)(tok - (long long)b * p.T);
+        b = (int)seq;
+        t = (int)in_seq;
         n = p.n_tokens ? p.n_tokens[b] : p.T;
-        koff = b * p.kl.seq + t * p.kl.token;
-        voff = b * p.vl.seq + t * p.vl.token;
     }
     const SeqInfo s = seq_info(c, p.rows[b], n, p.cu ? 0x7fffffff : p.T, t == 0 && lane == 0);
     if (!s.ok || t >= n) return;
@@ -525,13 +543,18 @@ __global__ void __launch_bounds__(256) kda_kv_append_kernel(const AppendParams p
     constexpr int ES = E4M3 ? 1 : 2;
     const size_t row = (size_t)c.D * ES, head = row * c.ps;
     const size_t at = ((size_t)p.layer * c.pages + page) * c.page_bytes() + (pos & (c.ps - 1)) * row;
-    const int per_log2 = c.D == 128 ? 4 : 3, pieces = c.Hkv << per_log2;   // 8 elements each
-#pragma unroll 4
-    for (int q = lane; q < pieces; q += 32) {
+    auto put = [&](int q, const uint4 &kx, const uint4 &vx) {
         const int h = q >> per_log2, i = q & ((1 << per_log2) - 1);
         const size_t to = at + h * head + (size_t)i * 8 * ES;
-        append_piece<E4M3, F16>(p.k + koff + h * p.kl.head + i * 8, c.k + to, E4M3 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
-        append_piece<E4M3, F16>(p.v + voff + h * p.vl.head + i * 8, c.v + to, E4M3 ? c.v_scale[p.layer * c.Hkv + h] : 1.f);
+        append_piece<E4M3, F16>(kx, c.k + to, E4M3 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
+        append_piece<E4M3, F16>(vx, c.v + to, E4M3 ? c.v_scale[p.layer * c.Hkv + h] : 1.f);
+    };
+#pragma unroll
+    for (int a = 0; a < kAhead; a++)
+        if (lane + 32 * a < pieces) put(lane + 32 * a, kw[a], vw[a]);
+    for (int q = lane + 32 * kAhead; q < pieces; q += 32) {
+        const int h = q >> per_log2, i = q & ((1 << per_log2) - 1);
+        put(q, __ldcs(reinterpret_cast<const uint4 *>(ks + h * p.kl.head + i * 8)), __ldcs(reinterpret_cast<const uint4 *>(vs + h * p.vl.head + i * 8)));
     }
 }
 
@@ -552,7 +575,7 @@ cudaError_t launch_kv_extend(const KvCall &p, cudaStream_t stream)
     cudaError_t e = paged_sm_count(&sms);
     if (e == cudaSuccess) e = setup.get(kda_kv_extend_kernel, kNt, kMaxMaps, 0, nullptr);
     if (e == cudaSuccess) e = launch_pdl_cluster(kda_kv_extend_kernel, dim3(kCl), dim3(kNt), smem, kCl, stream, p);
-    if (e == cudaSuccess) e = launch_pdl(kda_kv_copy_tails_kernel, dim3((unsigned)sms), dim3(256), 0, stream, p);
+    if (e == cudaSuccess) e = launch_pdl(kda_kv_copy_tails_kernel, dim3((unsigned)sms * 4), dim3(256), 0, stream, p);
     return e;
 }
 
