@@ -147,7 +147,9 @@ def _call(device: torch.device, fn, *args) -> None:
     current device (and takes per-device set-up from it), which must be the one that owns the
     pointers."""
     if torch.cuda.current_device() == device.index:
-        _raise(fn(*args))
+        st = fn(*args)
+        if st != KDA_OK:
+            _raise(st)
     else:
         with torch.cuda.device(device):
             _raise(fn(*args))

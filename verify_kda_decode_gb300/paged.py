@@ -288,17 +288,18 @@ def _attn(cache: KdaKvCache, q, packed: bool, scale, window, sinks, out, lse, re
     def make():
         ql = _tokens(q, "q", packed, None, cache)
         D = cache.head_dim
-        return ctypes.byref(_Desc(shape[-2], 1.0 / math.sqrt(D) if scale is None else float(scale), int(window), int(sinks), ql))
+        desc = _Desc(shape[-2], 1.0 / math.sqrt(D) if scale is None else float(scale), int(window), int(sinks), ql)
+        return ctypes.byref(desc), shape[:-1]
 
-    desc = _plan(cache, ("attn", packed, scale, window, sinks, q.dtype, q.device, shape, q.stride()), make)
+    desc, rows_shape = _plan(cache, ("attn", packed, scale, window, sinks, q.dtype, q.device, shape, q.stride()), make)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need(out, "out", q.dtype, shape, q.device)
     if lse is not None:
-        _need(lse, "lse", torch.float32, shape[:-1], q.device)
+        _need(lse, "lse", torch.float32, rows_shape, q.device)
     elif return_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lse = torch.empty(rows_shape, dtype=torch.float32, device=q.device)
     return desc, out, lse
 
 
