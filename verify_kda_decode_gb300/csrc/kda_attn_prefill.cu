@@ -77,6 +77,8 @@ struct Smem {
 struct Args {
     AttnParams p;
     CUtensorMap k, v;   // [layers pages][Hkv page_size][D], boxes of one page's tokens x 64 head dims
+    CUtensorMap q;      // [tokens][heads][D], boxes of 128 rows (token, head of the group) x 64 head dims
+    bool q_map;         // ... which need a group that divides 128
 };
 
 // Byte offset of 16-byte chunk g (of the row's D / 8) of row r in a tile.
@@ -346,9 +348,21 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
         return __ldg(c.table + (size_t)u.row * c.width + (k0 >> c.ps_log2));
     };
     int pages = pages_of(0), pages_next = pages_of(1);
-    // queries: 16 (or 8) lanes for a row; rows past the unit's are zeros
+    // queries; without a map 16 (or 8) lanes for a row, zeros past the unit's rows (the copies of 64 KiB by
+    // threads took 11000 clocks, longer than the sums they are to overlap)
     auto load_queries = [&]() {
         if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
+        if (args.q_map) {   // by TMA; rows past the unit's are other tokens' (or zeros), and what comes of them is not stored
+            if (tid == 0) mbar_arrive_expect_tx(&sm.q_full, u.halves * (kHalf * D * 2));
+            else mbar_arrive(&sm.q_full);
+            __syncwarp();
+            if (tid < u.halves * (D / 64)) {
+                const int hf = tid / (D / 64), x = tid % (D / 64);
+                tma_load_3d(smem_u32(sm.q[0]) + hf * (kHalf * D * 2) + x * kHalfBytes, &args.q, x * 64, u.h * p.G,
+                            u.c0 + (u.r0 + hf * kHalf) / p.G, &sm.q_full);
+            }
+            return true;
+        }
         constexpr int LPR = D / 8, STEP = kLoaders / LPR;   // lanes of a row, rows of a pass
         const int g = tid % LPR, step_t = STEP / p.G, step_q = STEP - step_t * p.G;
         int r = tid / LPR, t = (u.r0 + r) / p.G, q = u.r0 + r - t * p.G;   // the row's token and head of the group
@@ -368,6 +382,7 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
         return true;
     };
     auto queries_done = [&]() {
+        if (args.q_map) return;
         cp_async_wait_all();
         tc::fence_smem_to_async();
         mbar_arrive(&sm.q_full);
@@ -926,17 +941,30 @@ EncodeTiled encoder()
     return fn;
 }
 
-cudaError_t encode(CUtensorMap *map, void *base, const PagedCache &c)
+cudaError_t encode(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3])
 {
     const EncodeTiled fn = encoder();
     if (!fn) return cudaErrorSymbolNotFound;
-    const cuuint64_t row = (cuuint64_t)c.D * 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)c.Hkv * c.ps, (cuuint64_t)c.layers * c.pages};
-    const cuuint64_t strides[2] = {row, row * c.Hkv * c.ps};
-    const cuuint32_t box[3] = {64, (cuuint32_t)c.ps, 1}, step[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_pages(CUtensorMap *map, const void *base, const PagedCache &c)
+{
+    const cuuint64_t row = (cuuint64_t)c.D * 2;
+    return encode(map, base, {(cuuint64_t)c.D, (cuuint64_t)c.Hkv * c.ps, (cuuint64_t)c.layers * c.pages}, {row, row * c.Hkv * c.ps},
+                  {64, (cuuint32_t)c.ps, 1});
+}
+
+// (a dimension of one element may come with any stride, 0 too: its stride is not used)
+cudaError_t encode_queries(CUtensorMap *map, const AttnParams &p)
+{
+    const cuuint64_t row = (cuuint64_t)p.c.D * 2, head = p.Hq > 1 ? (cuuint64_t)p.ql.head * 2 : row,
+                     token = p.total > 1 ? (cuuint64_t)p.ql.token * 2 : row * p.Hq;
+    return encode(map, p.q, {(cuuint64_t)p.c.D, (cuuint64_t)p.Hq, (cuuint64_t)p.total}, {head, token},
+                  {64, (cuuint32_t)p.G, (cuuint32_t)(kHalf / p.G)});
 }
 
 template <int D, typename Q, bool FP8>
@@ -958,7 +986,10 @@ cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
     const int splits = units * 2 <= most ? (int)(most / units) : 1;
     Args a = {};
     a.p = p;
-    if (!FP8 && ((e = encode(&a.k, p.c.k, p.c)) != cudaSuccess || (e = encode(&a.v, p.c.v, p.c)) != cudaSuccess)) return e;
+    if (!FP8 && ((e = encode_pages(&a.k, p.c.k, p.c)) != cudaSuccess || (e = encode_pages(&a.v, p.c.v, p.c)) != cudaSuccess)) return e;
+    // heads or tokens that share memory (stride 0) and strides past the map's 40 bits take the copies
+    a.q_map = kHalf % p.G == 0 && (p.Hq == 1 || (p.ql.head > 0 && p.ql.head < 1ll << 38)) && (p.total == 1 || (p.ql.token > 0 && p.ql.token < 1ll << 38));
+    if (a.q_map && (e = encode_queries(&a.q, p)) != cudaSuccess) return e;
     a.p.splits = splits;
     const long long ctas = units * splits < sms ? units * splits : sms;
     return launch_pdl(kda_attn_prefill_kernel<D, Q, FP8>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a);
