@@ -57,6 +57,7 @@ struct Unit {
     int row, h;            // cache row, key head
     int c0, n, len;        // first packed token, new tokens, row length
     int r0, rows, halves;
+    int t0, g0;            // token and head of the group of row r0
     int p_first, p_last;   // positions of its first and last token
     int ta, tb, pieces;    // pieces > 1: the keys are split
 };
@@ -512,17 +513,24 @@ struct SplitWs {   // partial results of split units: (m, l) and O by column, so
     __device__ float *slot(int s, int D) const { return data + (size_t)s * slot_floats(D); }
 };
 
+// Token (of the unit's sequence) and index in [token, head] of a unit's row x.  The quotient comes from the
+// reciprocal: (g0 + x + 1/2) / G is at least 1 / (2 G) from a whole number, far more than the product's error.
+__device__ __forceinline__ int row_token(const AttnParams &p, const Unit &u, int x) { return u.t0 + (int)((u.g0 + x + 0.5f) * p.inv_g); }
+__device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, int x)
+{
+    const int t = row_token(p, u, x);
+    return (size_t)(u.c0 + t) * p.Hq + u.h * p.G + (u.r0 + x - t * p.G);
+}
+
 // 32 outputs of a row.  A warp's rows are apart, so each store instruction goes to 32 lines: whole 32-byte
 // sectors where the output's alignment allows it, which halves their number.
 template <typename Q>
-__device__ __forceinline__ void store_row(const AttnParams &p, const Unit &u, int r, int d, const float *o, float f)
+__device__ __forceinline__ void store_row(uint16_t *dst, bool wide, const float *o, float f)
 {
-    const int t = r / p.G, tok = u.c0 + t, hq = u.h * p.G + r - t * p.G;
-    uint16_t *dst = p.out + ((size_t)tok * p.Hq + hq) * p.c.D + d;
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; i++) w[i] = Q::pack(o[2 * i] * f, o[2 * i + 1] * f);
-    if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+    if (wide) {
 #pragma unroll
         for (int i = 0; i < 2; i++)
             asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -533,12 +541,14 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Unit &u, in
         for (int i = 0; i < 4; i++) reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
 }
+__device__ __forceinline__ bool wide_stores(const AttnParams &p) { return (reinterpret_cast<uintptr_t>(p.out) & 31) == 0; }
 
 // One row of a split unit from its pieces; `at`: the first piece's m of this row
 template <int D, typename Q, bool FP8>
 __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const float *at)
 {
-    const int r = u.r0 + threadIdx.x;
+    const size_t row = row_index(p, u, threadIdx.x);
+    uint16_t *dst = p.out + row * D;
     constexpr size_t step = SplitWs::slot_floats(D);
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < u.pieces; i++) m = fmaxf(m, __ldcg(at + i * step));
@@ -554,9 +564,9 @@ __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const 
 #pragma unroll
             for (int j = 0; j < 32; j++) o[j] += a * __ldcg(at + i * step + (size_t)(2 + d + j) * kRowsCta);
         }
-        store_row<Q>(p, u, r, d, o, f);
+        store_row<Q>(dst + d, wide_stores(p), o, f);
     }
-    if (p.lse) p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far)
@@ -568,14 +578,14 @@ __device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, ui
     const int tid = threadIdx.x, h = tid >> 7, rl = tid & 127, w = tid >> 5;
     const int n = u.tb - u.ta;
     const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
-    const int r = u.r0 + h * kHalf + rl;                         // row of the sequence
-    const bool live = h * kHalf + rl < u.rows;
+    const int x = h * kHalf + rl;                                // row of the unit
+    const bool live = x < u.rows;
     const float sc = fmaxf(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f), 1e-37f);
     const int first = u.len - u.n;
-    const int pos = first + min(r, u.n * p.G - 1) / p.G;          // this row's position
+    const int pos = first + row_token(p, u, min(x, u.rows - 1));  // this row's position
     const int lo = (int)max(-0x7fffffffll, (long long)pos - W + 1);
     // positions of the half's first and last row: whether a tile is seen by all of it
-    const int p_lo = first + (u.r0 + h * kHalf) / p.G, p_hi = first + min(u.r0 + h * kHalf + kHalf - 1, u.n * p.G - 1) / p.G;
+    const int p_lo = first + row_token(p, u, h * kHalf), p_hi = first + row_token(p, u, min(h * kHalf + kHalf, u.rows) - 1);
     const long long lo_all = (long long)p_hi - W + 1;
     const uint32_t lane_base = tmem + ((uint32_t)(w & 3) * 32u << 16);
     const uint32_t ts = lane_base + Cols<D>::s(h), tp = lane_base + Cols<D>::p(h), to = lane_base + Cols<D>::o(h);
@@ -646,6 +656,9 @@ __device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, ui
     tiles += n;
     units++;
     const float f = l == 0.f ? 0.f : (FP8 ? c.v_scale[p.layer * c.Hkv + u.h] : 1.f) / l;
+    const size_t row = row_index(p, u, x);
+    uint16_t *dst = p.out + row * D;
+    const bool wide = wide_stores(p);
 #pragma unroll 1
     for (int q = 0; q < D / 32; q++) {
         uint32_t v[32];
@@ -654,14 +667,14 @@ __device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, ui
 #pragma unroll
             for (int j = 0; j < 32; j++) __stcg(partial + (2 + 32 * q + j) * kRowsCta + tid, __uint_as_float(v[j]));
         } else if (live) {
-            store_row<Q>(p, u, r, 32 * q, reinterpret_cast<const float *>(v), f);
+            store_row<Q>(dst + 32 * q, wide, reinterpret_cast<const float *>(v), f);
         }
     }
     if (partial) {
         __stcg(partial + tid, m);
         __stcg(partial + kRowsCta + tid, l);
     } else if (live && p.lse) {
-        p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
     return true;
 }
@@ -689,9 +702,9 @@ __device__ void softmax_role(Smem<D> &sm, const AttnParams &p, uint32_t tmem, in
         if (u.tb == u.ta) {   // no token of the row tile sees a key
             if (tid < u.rows) {
                 const float z[32] = {};
-                const int r = u.r0 + tid;
-                for (int d = 0; d < D; d += 32) store_row<Q>(p, u, r, d, z, 0.f);
-                if (p.lse) p.lse[(size_t)(u.c0 + r / p.G) * p.Hq + u.h * p.G + r % p.G] = -INFINITY;
+                const size_t row = row_index(p, u, tid);
+                for (int d = 0; d < D; d += 32) store_row<Q>(p.out + row * D + d, false, z, 0.f);
+                if (p.lse) p.lse[row] = -INFINITY;
             }
         } else {
             if (h < u.halves && !softmax_unit<D, Q, FP8>(sm, p, u, tmem, W, S, partial, tiles, units)) return;
@@ -795,9 +808,11 @@ __device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
             u.n = s.n;
             u.len = s.len;
             u.r0 = tile * kRowsCta;
+            u.t0 = u.r0 / p.G;
+            u.g0 = u.r0 - u.t0 * p.G;
             u.rows = min(kRowsCta, u.n * p.G - u.r0);
             u.halves = u.rows > kHalf ? 2 : 1;
-            u.p_first = u.len - u.n + u.r0 / p.G;
+            u.p_first = u.len - u.n + u.t0;
             u.p_last = u.len - u.n + (u.r0 + u.rows - 1) / p.G;
             const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
             // this split's share of the key tiles, two at least; splits past the last piece have none
@@ -991,6 +1006,7 @@ cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
     a.q_map = kHalf % p.G == 0 && (p.Hq == 1 || (p.ql.head > 0 && p.ql.head < 1ll << 38)) && (p.total == 1 || (p.ql.token > 0 && p.ql.token < 1ll << 38));
     if (a.q_map && (e = encode_queries(&a.q, p)) != cudaSuccess) return e;
     a.p.splits = splits;
+    a.p.inv_g = 1.f / p.G;
     const long long ctas = units * splits < sms ? units * splits : sms;
     return launch_pdl(kda_attn_prefill_kernel<D, Q, FP8>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a);
 }
