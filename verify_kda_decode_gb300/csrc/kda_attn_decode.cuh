@@ -1,4 +1,4 @@
-// kda_attn_decode.cu -- attention of a few new tokens per sequence over a paged key-value cache
+// kda_attn_decode.cuh -- attention of a few new tokens per sequence over a paged key-value cache
 // (kda_attn_decode): decode, draft verify and mixed steps.
 //
 // Mathematics.  For one sequence and key head the rows are the call's (token, query head) pairs,
@@ -20,6 +20,8 @@
 //
 // Rows of a page that no token sees are not read: cp.async writes zeros for them, so whatever the
 // page holds there (NaN included) cannot reach the products.
+#pragma once
+
 #include "kda_attn_common.cuh"
 
 namespace kda {
@@ -223,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
     float *mg = reinterpret_cast<float *>(smem + C::Q_BYTES);          // merge buffer: O [warp][ROWS][D], m, l [warp][ROWS]
     float *mg_m = mg + kWarps * ROWS * D, *mg_l = mg_m + kWarps * ROWS;
 
+    int pages_of = -1, first_now = -1, first_next = -1;   // whose pages of tiles 0 to 63 this lane holds
     long long at = begin;
     while (at < end) {
         while (at >= prefix + seq_tiles) {   // next sequence with work (there is one: at < total)
@@ -252,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         uint32_t qf[C::Q_SMEM ? 1 : D / 16][2];
         float sc[NB][2];      // scale of rows 2 cc, 2 cc + 1, in log2 units
         int row_pos[NB][2];   // and their tokens' positions
-        const float sc_head = p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
+        // (a scale of 0 as the least that keeps hidden scores at -inf)
+        const float sc_head = fmaxf(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f), 1e-37f);
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = nb * 8 + g;
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             }
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                sc[nb][i] = sc_head * (FP8 && !Q::is_half ? __shfl_sync(~0u, up, 4 * (2 * cc + i)) : 1.f);
+                sc[nb][i] = fmaxf(sc_head * (FP8 && !Q::is_half ? __shfl_sync(~0u, up, 4 * (2 * cc + i)) : 1.f), 1e-37f);
                 row_pos[nb][i] = p0 + (mb * ROWS + nb * 8 + 2 * cc + i) / p.G;
             }
 #pragma unroll
@@ -325,11 +329,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         auto step_used = [&](int k0) { return k0 < kr.end && (k0 + kStep > kr.lo || k0 < S); };
         auto load_pages = [&](int t0) {
             const int t = t0 + lane;
-            if (t >= tb) return -1;
+            if (t >= kt) return -1;
             const int k0 = key_of(t);
             return step_used(k0) ? __ldg(c.table + (size_t)seq.row * c.width + (k0 >> c.ps_log2)) : -1;
         };
-        int pages_at = ta, pages_now = load_pages(ta), pages_next = load_pages(ta + 32);
+        // a sequence's next unit (another head, the same pages) begins with those of its last one
+        int pages_at = ta, pages_now, pages_next;
+        if (ta == 0 && pages_of == b) pages_now = first_now, pages_next = first_next;
+        else {
+            pages_now = load_pages(ta);
+            pages_next = load_pages(ta + 32);
+            if (ta == 0) pages_of = b, first_now = pages_now, first_next = pages_next;
+        }
 
         uint32_t bad = 0;   // bit s: the step in stage s has no page
         auto issue = [&](int t, int stage) {
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             st_out = st_out + 1 == C::NS ? 0 : st_out + 1;
             if (step_used(k0) && !(bad >> stage & 1)) {
                 const uint32_t kb = ring + stage * C::STAGE, vb = kb + kStep * C::RB;
-                float s[NB][4], s2[NB][4];   // two chains of products, added at the end
+                float s[NB][4], s2[NB][4];   // one row block: two chains of products, added at the end
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++)
 #pragma unroll
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                         uint2 q;
                         if constexpr (C::Q_SMEM) q = lds64(q_at + (nb * (D / 16) + kb_) * 256);
                         else q = make_uint2(qf[kb_][0], qf[kb_][1]);
-                        mma16816<P>(kb_ & 1 ? s2[nb] : s[nb], a, q.x, q.y);
+                        mma16816<P>(NB == 1 && (kb_ & 1) ? s2[nb] : s[nb], a, q.x, q.y);
                     }
                 };
 #pragma unroll
@@ -428,11 +439,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                 for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        s[nb][i] = (s[nb][i] + s2[nb][i]) * sc[nb][i & 1];
+                        if constexpr (NB == 1) s[nb][i] += s2[nb][i];
                         if (!all && !key_visible(k0 + g + 8 * (i >> 1), row_pos[nb][i & 1], W, S)) s[nb][i] = -INFINITY;
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; i++) grown |= fmaxf(s[nb][i], s[nb][i + 2]) > row_m[nb][i] + 8.f;
+                    for (int i = 0; i < 2; i++) grown |= fmaxf(s[nb][i], s[nb][i + 2]) * sc[nb][i] > row_m[nb][i] + 8.f;
                 }
                 if (__any_sync(~0u, grown)) {
 #pragma unroll
@@ -442,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                             float mx = fmaxf(s[nb][i], s[nb][i + 2]);
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-                            const float m_new = fmaxf(row_m[nb][i], mx);
+                            const float m_new = fmaxf(row_m[nb][i], mx * sc[nb][i]);
                             const float alpha = m_new == -INFINITY ? 1.f : ex2(row_m[nb][i] - m_new);
                             row_m[nb][i] = m_new;
                             row_l[nb][i] *= alpha;
@@ -456,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
                         const float base = row_m[nb][i] == -INFINITY ? 0.f : row_m[nb][i];   // a row that has seen no key yet
-                        s[nb][i] = ex2(s[nb][i] - base);
-                        s[nb][i + 2] = ex2(s[nb][i + 2] - base);
+                        s[nb][i] = ex2(fmaf(s[nb][i], sc[nb][i], -base));
+                        s[nb][i + 2] = ex2(fmaf(s[nb][i + 2], sc[nb][i], -base));
                         row_l[nb][i] += s[nb][i] + s[nb][i + 2];
                     }
                     // P is rounded to the product's 16-bit type (relative error 2^-9 or 2^-12, as the
@@ -653,14 +664,17 @@ cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
     return launch_pdl(kda_attn_decode_kernel<D, Q, FP8, NB>, dim3((unsigned)min(resident, kMaxCtas)), dim3(kThreads), smem, stream, p);
 }
 
-// Row blocks of 8, 16 or 32: the smallest that holds the rows of a sequence and key head, at most 32
-// (more rows read the keys again from L2).
+// Row blocks of 8, 16, 24 or 32: the smallest that holds the rows of a sequence and key head, at most 32
+// (more rows read the keys again from L2).  A step's instructions grow with the block: 20 rows, 64 sequences in
+// a 1024 window: 41 us with 32, 36 us with 24 (and without the second
+// chain of products and the separate scaling that both had).
 template <int D, typename Q, bool FP8>
 cudaError_t launch_rows(const AttnParams &p, cudaStream_t stream)
 {
     const int rows = p.T * p.G;
     if (rows <= 8) return launch_as<D, Q, FP8, 1>(p, stream);
     if (rows <= 16) return launch_as<D, Q, FP8, 2>(p, stream);
+    if (rows <= 24) return launch_as<D, Q, FP8, 3>(p, stream);
     return launch_as<D, Q, FP8, 4>(p, stream);
 }
 
@@ -672,12 +686,4 @@ cudaError_t launch_types(const AttnParams &p, cudaStream_t stream)
 }
 
 }  // namespace
-
-size_t attn_decode_workspace(int D) { return Partials::kCounters * sizeof(int) + 2 * kMaxCtas * Partials::slot_floats(D) * sizeof(float); }
-
-cudaError_t launch_attn_decode(const AttnParams &p, cudaStream_t stream)
-{
-    return p.c.D == 128 ? launch_types<128>(p, stream) : launch_types<64>(p, stream);
-}
-
 }  // namespace kda

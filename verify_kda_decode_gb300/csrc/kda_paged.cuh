@@ -1,5 +1,5 @@
 // kda_paged.cuh -- the paged key-value cache as the kernels see it, and the launchers of the
-// kernels that work on it (kda_kv.cu, kda_attn_decode.cu, kda_attn_prefill.cu).
+// kernels that work on it (kda_kv.cu, kda_attn_decode.cuh, kda_attn_prefill.cu).
 #pragma once
 
 #include "kda_internal.cuh"
@@ -75,7 +75,8 @@ struct AttnParams {
 // The attention workspace begins with counters (int, all 0 between calls), which both kernels use, then
 // holds partial results.
 constexpr size_t kAttnCounters = 4096;
-cudaError_t launch_attn_decode(const AttnParams &p, cudaStream_t stream);
+cudaError_t launch_attn_decode64(const AttnParams &p, cudaStream_t stream);
+cudaError_t launch_attn_decode128(const AttnParams &p, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const AttnParams &p, cudaStream_t stream);
 size_t attn_decode_workspace(int D);
 size_t attn_prefill_workspace(int D);

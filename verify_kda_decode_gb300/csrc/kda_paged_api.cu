@@ -313,7 +313,8 @@ kda_status kda_attn_decode(const kda_kv_cache *cache, int32_t layer, const kda_a
     CHECK(check_attn_workspace(cache, workspace, workspace_bytes));
     kda::AttnParams p = attn_params(cache, layer, desc, rows, B, T, q, out, lse, workspace);
     p.n_tokens = n_tokens;
-    return launched(kda::launch_attn_decode(p, static_cast<cudaStream_t>(stream)));
+    return launched(p.c.D == 64 ? kda::launch_attn_decode64(p, static_cast<cudaStream_t>(stream))
+                               : kda::launch_attn_decode128(p, static_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_attn_prefill(const kda_kv_cache *cache, int32_t layer, const kda_attn_desc *desc, const int32_t *rows,
