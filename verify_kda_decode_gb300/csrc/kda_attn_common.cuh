@@ -48,20 +48,43 @@ struct Bf16 {
     }
 };
 
-// Two E4M3 codes (low half first) -> two halves; exact.
-__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t w, int hi)
+// Four E4M3 codes -> four halves in order; exact.
+__device__ __forceinline__ void e4m3x4_half4(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(hi ? w >> 16 : w & 0xffffu), __NV_E4M3);
-    return (uint32_t)r.x | ((uint32_t)r.y << 16);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
 }
-// ... -> two values of the query's type; exact in both.
-template <typename Q>
-__device__ __forceinline__ uint32_t e4m3x2_as(uint32_t w, int hi)
+
+// With an E4M3 cache the products are taken in halves.  A bfloat16 row of queries is brought to a maximum in
+// [1, 2) by a power of two first (exact but for elements under 2^-14 of it, whose error stays under 2^-25 of
+// it): `mag` is the row's largest magnitude's bits; returns the factor `down` for the elements and `up` for
+// the scores.  Rows with infinities or NaN stay as they are.
+__device__ __forceinline__ void query_scale(uint32_t mag, float &down, float &up)
 {
-    const uint32_t h = e4m3x2_half2(w, hi);
-    if constexpr (Q::is_half) return h;
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    return Bf16::pack(f.x, f.y);
+    const int ex = (int)(mag >> 7);                              // biased exponent
+    const int e = ex == 255 ? 0 : min(max(ex, 1) - 127, 126);
+    down = __uint_as_float((uint32_t)(127 - e) << 23);
+    up = __uint_as_float((uint32_t)max(127 + e, 1) << 23);
+}
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, const uint4 &x)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t y = (&x.x)[i];
+        m = max(m, max(y & 0x7fffu, (y >> 16) & 0x7fffu));
+    }
+    return m;
+}
+// Eight bfloat16 -> eight halves, times `down`.
+__device__ __forceinline__ uint4 scaled_halves(const uint4 &x, float down)
+{
+    uint4 r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t y = (&x.x)[i];
+        (&r.x)[i] = Half::pack(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xffff0000u) * down);
+    }
+    return r;
 }
 
 template <int N>

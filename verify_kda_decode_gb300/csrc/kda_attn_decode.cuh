@@ -114,13 +114,6 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Four E4M3 codes -> four halves in order; exact.
-__device__ __forceinline__ void e4m3x4_half4(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-}
-
 __device__ __forceinline__ void cp16(uint32_t dst, const uint8_t *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -249,9 +242,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         const uint32_t dst_k = (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_k(lane / C::CH)) * 16);
         const uint32_t dst_v = (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_v(lane / C::CH)) * 16);
 
-        // queries: rows nb * 8 + g, the elements this thread multiplies.  With an E4M3 cache the products are
-        // taken in halves: a bfloat16 row is brought to a maximum in [1, 2) by a power of two first (exact
-        // but for elements under 2^-14 of it, whose error stays under 2^-25 of it)
+        // queries: rows nb * 8 + g, the elements this thread multiplies
         uint32_t qf[C::Q_SMEM ? 1 : D / 16][2];
         float sc[NB][2];      // scale of rows 2 cc, 2 cc + 1, in log2 units
         int row_pos[NB][2];   // and their tokens' positions
@@ -271,27 +262,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             }
             float up = 1.f;
             if constexpr (FP8 && !Q::is_half) {
-                uint32_t mx = 0;   // largest magnitude's bits
+                uint32_t mag = 0;
 #pragma unroll
-                for (int j = 0; j < D / 32; j++)
+                for (int j = 0; j < D / 32; j++) mag = max_magnitude(mag, x[j]);
+                mag = max(mag, __shfl_xor_sync(~0u, mag, 1));
+                mag = max(mag, __shfl_xor_sync(~0u, mag, 2));
+                float down;
+                query_scale(mag, down, up);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint32_t y = (&x[j].x)[i];
-                        mx = max(mx, max(y & 0x7fffu, (y >> 16) & 0x7fffu));
-                    }
-                mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
-                mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
-                const int ex = (int)(mx >> 7);                          // biased exponent
-                const int e = ex == 255 ? 0 : min(max(ex, 1) - 127, 126);   // infinite rows stay as they are
-                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                up = __uint_as_float((uint32_t)max(127 + e, 1) << 23);
-#pragma unroll
-                for (int j = 0; j < D / 32; j++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        uint32_t &y = (&x[j].x)[i];
-                        y = Half::pack(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xffff0000u) * down);
-                    }
+                for (int j = 0; j < D / 32; j++) x[j] = scaled_halves(x[j], down);
             }
 #pragma unroll
             for (int i = 0; i < 2; i++) {

@@ -43,7 +43,9 @@ constexpr int kHalf = 128, kRowsCta = 256, kKeys = 128;
 constexpr int kSoftmax = 256, kLoaders = 128, kThreads = kSoftmax + kLoaders + 128;
 // Registers of a thread: all start with 128 (512 threads, the whole file), then the softmax holds a row
 // of S at once, the loaders two fetches of E4M3 codes; 256 x 184 + 128 x 80 + 128 x 64 = 65536.
-constexpr int kRegs = 128, kRegsSoftmax = 184, kRegsLoad = 80, kRegsMma = 64;
+constexpr int kRegs = 128, kRegsMma = 64;
+template <bool FP8> constexpr int kRegsSoftmax = FP8 ? 176 : 184;
+template <bool FP8> constexpr int kRegsLoad = FP8 ? 96 : 80;
 constexpr uint32_t kSlots = 4;
 constexpr int kHalfBytes = kKeys * 128;   // a tile's 64 head dims: 128 rows of 128 bytes
 constexpr int kMaxSplitCtas = 256;             // CTAs of a launch whose keys are split
@@ -66,10 +68,11 @@ template <int D>
 struct Smem {
     uint8_t q[2][kHalf * D * 2];
     uint8_t kv[kSlots][kKeys * D * 2];
-    uint64_t q_full, q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
+    uint64_t q_full[2], q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
     Unit unit[kUnits];
     int before[kTable + 1], warp_sum[16];   // row tiles of the sequences before each one
     int4 seq[kTable];                       // row, length, new tokens, first packed token
+    float q_scale[2][kRowsCta];             // E4M3 cache: what a unit's scores have to be multiplied with, by its parity
     uint32_t tmem;
     int last;
     volatile int stop;
@@ -122,7 +125,8 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-static_assert(kSoftmax * kRegsSoftmax + kLoaders * kRegsLoad + 128 * kRegsMma <= kThreads * kRegs, "setmaxnreg would wait forever");
+static_assert(kSoftmax * kRegsSoftmax<false> + kLoaders * kRegsLoad<false> + 128 * kRegsMma <= kThreads * kRegs &&
+              kSoftmax * kRegsSoftmax<true> + kLoaders * kRegsLoad<true> + 128 * kRegsMma <= kThreads * kRegs, "setmaxnreg would wait forever");
 
 __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1)
 {
@@ -279,7 +283,7 @@ __device__ __forceinline__ bool issue_products(Smem<D> &sm, int n, uint32_t tmem
             }
         }
     };
-    if (!wait_warp(sm, &sm.q_full, units & 1, err)) return false;
+    if (!wait_warp(sm, &sm.q_full[units & 1], (units >> 1) & 1, err)) return false;
     if (!slot_wait(item)) return false;
     tc::fence_after_sync();
 #pragma unroll
@@ -327,6 +331,15 @@ __device__ void mma_role(Smem<D> &sm, uint32_t tmem, int *err)
     }
 }
 
+// Token (of the unit's sequence) and index in [token, head] of a unit's row x.  The quotient comes from the
+// reciprocal: (g0 + x + 1/2) / G is at least 1 / (2 G) from a whole number, far more than the product's error.
+__device__ __forceinline__ int row_token(const AttnParams &p, const Unit &u, int x) { return u.t0 + (int)((u.g0 + x + 0.5f) * p.inv_g); }
+__device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, int x)
+{
+    const int t = row_token(p, u, x);
+    return (size_t)(u.c0 + t) * p.Hq + u.h * p.G + (u.r0 + x - t * p.G);
+}
+
 // ---- warps 8-11: a unit's queries, then keys and values of tile i as ring items 2 i and 2 i + 1
 // (`item`: ring items so far, `units`: units so far)
 template <int D, typename Q, bool FP8>
@@ -353,14 +366,37 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
     // threads took 11000 clocks, longer than the sums they are to overlap)
     auto load_queries = [&]() {
         if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
+        if constexpr (FP8 && !Q::is_half) {   // through registers, as halves
+            constexpr int LPR = D / 8, STEP = kLoaders / LPR;
+            const int g = tid % LPR;
+            const uint16_t *base = p.q + (long long)u.c0 * p.ql.token + (long long)(u.h * p.G) * p.ql.head + g * 8;
+#pragma unroll 4
+            for (int i = 0; i < 2 * kHalf / STEP; i++) {
+                const int r = i * STEP + tid / LPR;
+                if (i * STEP >= u.halves * kHalf) break;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (r < u.rows) {
+                    const int t = row_token(p, u, r);
+                    x = __ldg(reinterpret_cast<const uint4 *>(base + t * p.ql.token + (u.r0 + r - t * p.G) * p.ql.head));
+                }
+                uint32_t mag = max_magnitude(0, x);
+#pragma unroll
+                for (int o = 1; o < LPR; o <<= 1) mag = max(mag, __shfl_xor_sync(~0u, mag, o));
+                float down, up;
+                query_scale(mag, down, up);
+                *reinterpret_cast<uint4 *>(sm.q[0] + (r >> 7) * (kHalf * D * 2) + chunk_at(r & 127, g)) = scaled_halves(x, down);
+                if (g == 0) sm.q_scale[units & 1][r] = up;
+            }
+            return true;
+        }
         if (args.q_map) {   // by TMA; rows past the unit's are other tokens' (or zeros), and what comes of them is not stored
-            if (tid == 0) mbar_arrive_expect_tx(&sm.q_full, u.halves * (kHalf * D * 2));
-            else mbar_arrive(&sm.q_full);
+            if (tid == 0) mbar_arrive_expect_tx(&sm.q_full[units & 1], u.halves * (kHalf * D * 2));
+            else mbar_arrive(&sm.q_full[units & 1]);
             __syncwarp();
             if (tid < u.halves * (D / 64)) {
                 const int hf = tid / (D / 64), x = tid % (D / 64);
                 tma_load_3d(smem_u32(sm.q[0]) + hf * (kHalf * D * 2) + x * kHalfBytes, &args.q, x * 64, u.h * p.G,
-                            u.c0 + (u.r0 + hf * kHalf) / p.G, &sm.q_full);
+                            u.c0 + (u.r0 + hf * kHalf) / p.G, &sm.q_full[units & 1]);
             }
             return true;
         }
@@ -383,10 +419,10 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
         return true;
     };
     auto queries_done = [&]() {
-        if (args.q_map) return;
+        if (args.q_map && !(FP8 && !Q::is_half)) return;
         cp_async_wait_all();
         tc::fence_smem_to_async();
-        mbar_arrive(&sm.q_full);
+        mbar_arrive(&sm.q_full[units & 1]);
     };
     // source of this lane's key of group gi of tile i; null where nothing is read
     auto source = [&](const uint8_t *base, int i, int gi, int pg) -> const uint8_t * {
@@ -445,7 +481,7 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
         if (!load_queries()) return false;
         queries_done();
         // codes pass through registers: the next item's loads are in flight while this one's are
-        // converted (exactly) to the query's type and stored
+        // converted (exactly) to halves and stored
         uint4 cur[GR * PASS > 0 ? GR * PASS : 1], nxt[GR * PASS > 0 ? GR * PASS : 1];
         auto fetch = [&](int it, uint4 *v, int pg_lane) {
             const uint8_t *base = it & 1 ? c.v : c.k;
@@ -476,10 +512,13 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
                 for (int x = 0; x < PASS; x++) {
                     const uint4 v = cur[a * PASS + x];
                     const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t e[8];
+#pragma unroll
+                    for (int s = 0; s < 4; s++) e4m3x4_half4(ws[s], e[2 * s], e[2 * s + 1]);
 #pragma unroll
                     for (int s = 0; s < 2; s++)
                         *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at((w + 4 * a) * 8 + r8, (x * 4 + q4) * 2 + s)) =
-                            make_uint4(e4m3x2_as<Q>(ws[2 * s], 0), e4m3x2_as<Q>(ws[2 * s], 1), e4m3x2_as<Q>(ws[2 * s + 1], 0), e4m3x2_as<Q>(ws[2 * s + 1], 1));
+                            make_uint4(e[4 * s], e[4 * s + 1], e[4 * s + 2], e[4 * s + 3]);
                 }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.full[slot]);
@@ -512,15 +551,6 @@ struct SplitWs {   // partial results of split units: (m, l) and O by column, so
     static constexpr size_t slot_floats(int D) { return (size_t)kRowsCta * (D + 2); }
     __device__ float *slot(int s, int D) const { return data + (size_t)s * slot_floats(D); }
 };
-
-// Token (of the unit's sequence) and index in [token, head] of a unit's row x.  The quotient comes from the
-// reciprocal: (g0 + x + 1/2) / G is at least 1 / (2 G) from a whole number, far more than the product's error.
-__device__ __forceinline__ int row_token(const AttnParams &p, const Unit &u, int x) { return u.t0 + (int)((u.g0 + x + 0.5f) * p.inv_g); }
-__device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, int x)
-{
-    const int t = row_token(p, u, x);
-    return (size_t)(u.c0 + t) * p.Hq + u.h * p.G + (u.r0 + x - t * p.G);
-}
 
 // 32 outputs of a row.  A warp's rows are apart, so each store instruction goes to 32 lines: whole 32-byte
 // sectors where the output's alignment allows it, which halves their number.
@@ -569,10 +599,11 @@ __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const 
     if (p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far)
+// ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far; `all_units`:
+// those of either half)
 template <int D, typename Q, bool FP8>
 __device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
-                             uint32_t &tiles, uint32_t &units)
+                             uint32_t &tiles, uint32_t &units, uint32_t all_units)
 {
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, h = tid >> 7, rl = tid & 127, w = tid >> 5;
@@ -580,7 +611,15 @@ __device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, ui
     const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
     const int x = h * kHalf + rl;                                // row of the unit
     const bool live = x < u.rows;
-    const float sc = fmaxf(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f), 1e-37f);
+    using P = std::conditional_t<FP8, Half, Q>;                  // type of the products
+    float row_scale = 1.f;
+    if constexpr (FP8 && !Q::is_half) {
+        // (the barrier of this parity cannot move on again before this half's last scores of the unit are read)
+        if (!wait_warp(sm, &sm.q_full[all_units & 1], (all_units >> 1) & 1, c.err)) return false;
+        row_scale = sm.q_scale[all_units & 1][x];
+    }
+    // (a scale of 0 as the least that keeps hidden scores at -inf)
+    const float sc = fmaxf(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f) * row_scale, 1e-37f);
     const int first = u.len - u.n;
     const int pos = first + row_token(p, u, min(x, u.rows - 1));  // this row's position
     const int lo = (int)max(-0x7fffffffll, (long long)pos - W + 1);
@@ -641,7 +680,7 @@ __device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, ui
                 e0 = ex2(e0), e1 = ex2(e1);
                 if (j & 1) add2(s2, s3, e0, e1);
                 else add2(s0, s1, e0, e1);
-                v[j] = Q::pack(e0, e1);   // rounded to 16 bits for the product; l sums it unrounded
+                v[j] = P::pack(e0, e1);   // rounded to 16 bits for the product; l sums it unrounded
             }
             tmem_st32(tp + 32 * q, v + 32 * q);
         }
@@ -695,7 +734,7 @@ __device__ void softmax_role(Smem<D> &sm, const AttnParams &p, uint32_t tmem, in
     int *count = reinterpret_cast<int *>(p.ws);
     SplitWs ws;
     ws.data = reinterpret_cast<float *>(p.ws + kAttnCounters * sizeof(int));
-    uint32_t tiles = 0, units = 0, joins = 0;
+    uint32_t tiles = 0, units = 0, all_units = 0, joins = 0;
     for (int k = 0; const Unit *at = unit_of(sm, k, p.c.err); k++) {
         const Unit &u = *at;
         float *partial = u.pieces > 1 ? ws.slot(u.idx, D) : nullptr;
@@ -707,7 +746,8 @@ __device__ void softmax_role(Smem<D> &sm, const AttnParams &p, uint32_t tmem, in
                 if (p.lse) p.lse[row] = -INFINITY;
             }
         } else {
-            if (h < u.halves && !softmax_unit<D, Q, FP8>(sm, p, u, tmem, W, S, partial, tiles, units)) return;
+            if (h < u.halves && !softmax_unit<D, Q, FP8>(sm, p, u, tmem, W, S, partial, tiles, units, all_units)) return;
+            all_units++;
             if (partial) {
                 // the last of a unit's CTAs joins the pieces, in their order
                 const int splits = p.splits, first = u.idx / splits;
@@ -853,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
     if (tid == 0) {
-        mbar_init(&sm.q_full, kLoaders);
+        for (int i = 0; i < 2; i++) mbar_init(&sm.q_full[i], kLoaders);   // by the unit's parity
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.join, kSoftmax / 32);
         mbar_init(&sm.drain, 1);
@@ -908,18 +948,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
     }
     const uint32_t tmem = sm.tmem;
     if (warp < 8) {
-        regs_inc<kRegsSoftmax>();
+        regs_inc<kRegsSoftmax<FP8>>();
         softmax_role<D, Q, FP8>(sm, p, tmem, W, S);
         __syncwarp();
         regs_dec<kRegs>();   // back to what the common code was compiled for
     } else if (warp < 12) {
-        regs_dec<kRegsLoad>();
+        regs_dec<kRegsLoad<FP8>>();
         load_role<D, Q, FP8>(sm, args, W, S);
         __syncwarp();
         regs_inc<kRegs>();
     } else {
         regs_dec<kRegsMma>();
-        if (warp == 12) mma_role<D, Q>(sm, __reduce_max_sync(~0u, tmem), p.c.err);
+        if (warp == 12) mma_role<D, std::conditional_t<FP8, Half, Q>>(sm, __reduce_max_sync(~0u, tmem), p.c.err);
         else if (warp == 13) unit_role<D>(sm, p, W, S);
         __syncwarp();
         regs_inc<kRegs>();
