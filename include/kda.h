@@ -312,7 +312,7 @@ typedef struct {
     int32_t *seq_lens;       /* [rows] */
     int32_t *page_refs;      /* [num_pages] */
     const float *k_scale;    /* [num_layers, num_kv_heads], needed with KDA_T_E4M3 (else ignored): */
-    const float *v_scale;    /*   a stored code c stands for scale * c */
+    const float *v_scale;    /*   a stored code c stands for scale * c; >= 0 */
     int32_t *err_word;       /* device int32, zero-initialised by the caller */
 } kda_kv_cache;
 

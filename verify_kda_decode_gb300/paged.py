@@ -102,7 +102,8 @@ class KdaKvCache:
         """(struct, reference to it), checked and built once while the same storages are attached."""
         d = self.__dict__
         ptrs = (self.k.data_ptr(), self.v.data_ptr(), self.page_table.data_ptr(), self.seq_lens.data_ptr(),
-                self.page_refs.data_ptr(), self.err_word.data_ptr())
+                self.page_refs.data_ptr(), self.err_word.data_ptr(),
+                self.k_scale.data_ptr() if self.k_scale is not None else 0, self.v_scale.data_ptr() if self.v_scale is not None else 0)
         cached = d.get("_c_struct")
         if cached is not None and cached[2] == ptrs:
             return cached
