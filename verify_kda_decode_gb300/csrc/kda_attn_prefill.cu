@@ -48,20 +48,22 @@ template <bool FP8> constexpr int kRegsSoftmax = FP8 ? 176 : 184;
 template <bool FP8> constexpr int kRegsLoad = FP8 ? 96 : 80;
 constexpr uint32_t kSlots = 4;
 constexpr int kHalfBytes = kKeys * 128;   // a tile's 64 head dims: 128 rows of 128 bytes
-constexpr int kMaxSplitCtas = 256;             // CTAs of a launch whose keys are split
+constexpr int kMaxSplitCtas = 256;             // CTAs of a launch, and pieces of split units
+constexpr int kMaxSplits = 32;                 // pieces of a unit (their join reads one after the other)
 constexpr uint64_t kLimitNs = 2000000000ull;   // bound of every wait
 constexpr int kUnits = 2, kTable = 512;         // units on their way to the roles; sequences whose tile counts are kept on chip
 constexpr float kGrow = 8.f;                   // log2 growth of the maximum that O is rescaled for
 
 // What a CTA works on: rows [r0, r0 + rows) of the n * G of a sequence, and key tiles [ta, tb) of their range.
 struct Unit {
-    int idx;               // its number: (row tile, key head, split), -1: no more
+    int idx;               // its number, -1: no more
     int row, h;            // cache row, key head
     int c0, n, len;        // first packed token, new tokens, row length
     int r0, rows, halves;
     int t0, g0;            // token and head of the group of row r0
     int p_first, p_last;   // positions of its first and last token
     int ta, tb, pieces;    // pieces > 1: the keys are split
+    int slot, first, group;   // ... this piece's and the first one's place in the workspace, the split unit's number
 };
 
 template <int D>
@@ -737,7 +739,7 @@ __device__ void softmax_role(Smem<D> &sm, const AttnParams &p, uint32_t tmem, in
     uint32_t tiles = 0, units = 0, all_units = 0, joins = 0;
     for (int k = 0; const Unit *at = unit_of(sm, k, p.c.err); k++) {
         const Unit &u = *at;
-        float *partial = u.pieces > 1 ? ws.slot(u.idx, D) : nullptr;
+        float *partial = u.pieces > 1 ? ws.slot(u.slot, D) : nullptr;
         if (u.tb == u.ta) {   // no token of the row tile sees a key
             if (tid < u.rows) {
                 const float z[32] = {};
@@ -750,17 +752,16 @@ __device__ void softmax_role(Smem<D> &sm, const AttnParams &p, uint32_t tmem, in
             all_units++;
             if (partial) {
                 // the last of a unit's CTAs joins the pieces, in their order
-                const int splits = p.splits, first = u.idx / splits;
                 __threadfence();
                 if (!softmax_sync(sm, joins, p.c.err)) return;
                 if (tid == 0) {
-                    const int done = atomicAdd(count + first, 1);
+                    const int done = atomicAdd(count + u.group, 1);
                     sm.last = done == u.pieces - 1;
-                    if (sm.last) count[first] = 0;   // ready for the next call
+                    if (sm.last) count[u.group] = 0;   // ready for the next call
                     __threadfence();
                 }
                 if (!softmax_sync(sm, joins, p.c.err)) return;
-                if (sm.last && tid < u.rows) join_row<D, Q, FP8>(p, u, ws.slot(first * splits, D) + tid);
+                if (sm.last && tid < u.rows) join_row<D, Q, FP8>(p, u, ws.slot(u.first, D) + tid);
                 if (!softmax_sync(sm, joins, p.c.err)) return;   // sm.last is read
             }
         }
@@ -790,7 +791,7 @@ template <int D>
 __device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
 {
     const PagedCache &c = p.c;
-    const int lane = threadIdx.x & 31, splits = p.splits;
+    const int lane = threadIdx.x & 31;
     int *counter = reinterpret_cast<int *>(p.ws) + kMaxSplitCtas;   // next unit, CTAs that are done
     const int kept = min(p.B, kTable);
     int all = sm.before[kept];
@@ -799,14 +800,23 @@ __device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
         if (b0 + lane < p.B) t = (prefill_seq(p, b0 + lane, c0, blockIdx.x == 0).n * p.G + kRowsCta - 1) / kRowsCta;
         all += __reduce_add_sync(~0u, t);
     }
-    const long long total = (long long)all * c.Hkv * splits;
+    // Fewer units than CTAs: they are split over the keys.  (Splitting those of a partly filled last round as well
+    // costs more than it saves: 16384 tokens in a 2048 window, 512 units for 152 CTAs, 125 us against 122.)
+    const long long n_units = (long long)all * c.Hkv;
+    const int splits = n_units > 0 && n_units * 2 <= gridDim.x ? min(kMaxSplits, (int)(gridDim.x / n_units)) : 1;
+    const long long total = n_units * splits;
     long long idx = blockIdx.x;
     for (int k = 0;; k++) {
         const int slot = k % kUnits;
         Unit u;
         u.idx = -1;
         if (idx < total) {
-            const int y = (int)(idx % splits), x = (int)(idx / splits) / c.Hkv;
+            const long long unit = idx / splits;
+            const int y = (int)(idx - unit * splits), x = (int)(unit / c.Hkv);
+            u.h = (int)(unit - (long long)x * c.Hkv);
+            u.slot = (int)idx;         // (used where splits > 1: fewer than the CTAs then)
+            u.first = u.slot - y;
+            u.group = (int)unit;
             const int want = all - 1 - x;   // the last row tiles first: the longest of a causal prompt
             int b = -1, tile = 0;
             if (want < sm.before[kept]) {
@@ -843,7 +853,6 @@ __device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
             if (b < kept) s.row = sm.seq[b].x, s.len = sm.seq[b].y, s.n = sm.seq[b].z, u.c0 = sm.seq[b].w;
             else s = prefill_seq(p, b, u.c0, false);
             u.idx = (int)idx;
-            u.h = (int)(idx / splits) % c.Hkv;
             u.row = s.row;
             u.n = s.n;
             u.len = s.len;
@@ -856,7 +865,7 @@ __device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
             u.p_last = u.len - u.n + (u.r0 + u.rows - 1) / p.G;
             const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
             // this split's share of the key tiles, two at least; splits past the last piece have none
-            const int share = max(2, (kr.count + splits - 1) / splits);
+            const int share = splits > 1 ? max(2, (kr.count + splits - 1) / splits) : max(1, kr.count);
             u.pieces = max(1, (kr.count + share - 1) / share);
             u.ta = min(kr.count, y * share);
             u.tb = min(kr.count, u.ta + share);
@@ -1036,18 +1045,14 @@ cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
     const long long by_len = (long long)p.B * (((long long)p.T * p.G + kRowsCta - 1) / kRowsCta);
     const long long tiles = by_total < by_len ? by_total : by_len, units = tiles * p.c.Hkv;
     if (units > 0x7fffffffll) return cudaErrorInvalidValue;
-    // too few units to fill the SMs: split the keys
-    const int most = sms < kMaxSplitCtas ? sms : kMaxSplitCtas;
-    const int splits = units * 2 <= most ? (int)(most / units) : 1;
     Args a = {};
     a.p = p;
     if (!FP8 && ((e = encode_pages(&a.k, p.c.k, p.c)) != cudaSuccess || (e = encode_pages(&a.v, p.c.v, p.c)) != cudaSuccess)) return e;
     // heads or tokens that share memory (stride 0) and strides past the map's 40 bits take the copies
     a.q_map = kHalf % p.G == 0 && (p.Hq == 1 || (p.ql.head > 0 && p.ql.head < 1ll << 38)) && (p.total == 1 || (p.ql.token > 0 && p.ql.token < 1ll << 38));
     if (a.q_map && (e = encode_queries(&a.q, p)) != cudaSuccess) return e;
-    a.p.splits = splits;
     a.p.inv_g = 1.f / p.G;
-    const long long ctas = units * splits < sms ? units * splits : sms;
+    const int ctas = sms < kMaxSplitCtas ? sms : kMaxSplitCtas;
     return launch_pdl(kda_attn_prefill_kernel<D, Q, FP8>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a);
 }
 

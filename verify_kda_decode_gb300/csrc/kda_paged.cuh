@@ -64,7 +64,6 @@ struct AttnParams {
     int B, T;                      // decode: tokens per sequence; prefill: bound on a sequence's tokens
     int total;                     // prefill: packed tokens
     float inv_g;                   // prefill: 1 / G (set by the launcher)
-    int splits;                    // prefill: CTAs that share a unit's keys (set by the launcher)
     const uint16_t *q;
     TokensLayout ql;
     uint16_t *out;
