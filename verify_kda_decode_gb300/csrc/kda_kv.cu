@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(256) kda_kv_move_kernel(const KvCall p)
 // One warp per new token: lanes over the token's 16-byte source pieces (8 elements), keys then
 // values.  Pure data movement, bound by HBM for prompts and by the launch for a decode step.
 template <bool E4M3, bool F16>
-__device__ __forceinline__ void append_piece(const uint4 w, uint8_t *dst, float scale)
+__device__ __forceinline__ void append_piece(const uint4 w, uint8_t *dst, float2 scale)   // scale and its reciprocal
 {
     if constexpr (!E4M3) {
         *reinterpret_cast<uint4 *>(dst) = w;
@@ -452,21 +452,20 @@ __device__ __forceinline__ void append_piece(const uint4 w, uint8_t *dst, float 
         // The code is the rounding of the IEEE quotient.  Markstein's theorem gives that quotient from the correctly
         // rounded reciprocal: q = f r, then q + (f - q scale) r, three packed operations for two elements
         // (a division each took 57 us for 33000 tokens, bound by its instructions).  Infinities, and scales whose
-        // reciprocal or products could leave the normal range, take the division.
-        const float r = __frcp_rn(scale);
+        // reciprocal or products could leave the normal range (their reciprocal is given as NaN), take the
+        // division.
         float t0 = 0.f, t1 = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             float e0, e1;
-            tc::mul2(q[i], q[i + 1], f[i], f[i + 1], r, r);
-            tc::fma2(e0, e1, q[i], q[i + 1], -scale, -scale, f[i], f[i + 1]);
-            tc::fma2(q[i], q[i + 1], e0, e1, r, r, q[i], q[i + 1]);
+            tc::mul2(q[i], q[i + 1], f[i], f[i + 1], scale.y, scale.y);
+            tc::fma2(e0, e1, q[i], q[i + 1], -scale.x, -scale.x, f[i], f[i + 1]);
+            tc::fma2(q[i], q[i + 1], e0, e1, scale.y, scale.y, q[i], q[i + 1]);
             tc::add2(t0, t1, t0, t1, q[i], q[i + 1]);
         }
-        const float a = fabsf(scale);
-        if (!(a > 1e-18f && a < 1e18f) || !(fabsf(t0 + t1) < 1e30f)) {
+        if (!(fabsf(t0 + t1) < 1e30f)) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) q[i] = __fdiv_rn(f[i], scale);
+            for (int i = 0; i < 8; i++) q[i] = __fdiv_rn(f[i], scale.x);
         }
         uint32_t o[2];
 #pragma unroll
@@ -477,15 +476,27 @@ __device__ __forceinline__ void append_piece(const uint4 w, uint8_t *dst, float 
     }
 }
 
+// A scale and its correctly rounded reciprocal, NaN where quotients cannot be had from it.
+__device__ __forceinline__ float2 with_reciprocal(float scale)
+{
+    const float a = fabsf(scale);
+    return make_float2(scale, a > 1e-18f && a < 1e18f ? __frcp_rn(scale) : NAN);
+}
+
 template <bool E4M3, bool F16>
 __global__ void __launch_bounds__(256) kda_kv_append_kernel(const AppendParams p)
 {
+    constexpr int kScales = 64;   // key heads whose scales are kept on chip
+    __shared__ float2 scales[2][E4M3 ? kScales : 1];
     const PagedCache &c = p.c;
     const int lane = threadIdx.x & 31;
     const long long tok = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const long long tokens = p.cu ? p.T : (long long)p.B * p.T;
     grid_dependency_wait();
-    if (tok >= tokens) return;
+    auto scale = [&](int kv, int h) {
+        if constexpr (!E4M3) return make_float2(1.f, 1.f);
+        else return h < kScales ? scales[kv][h] : with_reciprocal((kv ? c.v_scale : c.k_scale)[p.layer * c.Hkv + h]);
+    };
     // The token's first pieces are on their way while its place is found, a chain of five loads (offsets, row,
     // length, page) that took longer than moving the data.
     const int per_log2 = c.D == 128 ? 4 : 3, pieces = c.Hkv << per_log2;   // 8 elements each
@@ -496,11 +507,17 @@ __global__ void __launch_bounds__(256) kda_kv_append_kernel(const AppendParams p
 #pragma unroll
     for (int a = 0; a < kAhead; a++) {
         const int q = lane + 32 * a, h = q >> per_log2, i = q & ((1 << per_log2) - 1);
-        if (q < pieces) {
+        if (tok < tokens && q < pieces) {
             kw[a] = __ldcs(reinterpret_cast<const uint4 *>(ks + h * p.kl.head + i * 8));
             vw[a] = __ldcs(reinterpret_cast<const uint4 *>(vs + h * p.vl.head + i * 8));
         }
     }
+    if constexpr (E4M3) {
+        for (int i = threadIdx.x; i < 2 * min(c.Hkv, kScales); i += 256)
+            scales[i & 1][i >> 1] = with_reciprocal(((i & 1) ? c.v_scale : c.k_scale)[p.layer * c.Hkv + (i >> 1)]);
+        __syncthreads();
+    }
+    if (tok >= tokens) return;
     int b, t, n;
     if (p.cu) {
         // the sequence whose offsets hold this row: the last b with cu[b] <= tok, 32 at a time
@@ -546,8 +563,8 @@ __global__ void __launch_bounds__(256) kda_kv_append_kernel(const AppendParams p
     auto put = [&](int q, const uint4 &kx, const uint4 &vx) {
         const int h = q >> per_log2, i = q & ((1 << per_log2) - 1);
         const size_t to = at + h * head + (size_t)i * 8 * ES;
-        append_piece<E4M3, F16>(kx, c.k + to, E4M3 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
-        append_piece<E4M3, F16>(vx, c.v + to, E4M3 ? c.v_scale[p.layer * c.Hkv + h] : 1.f);
+        append_piece<E4M3, F16>(kx, c.k + to, scale(0, h));
+        append_piece<E4M3, F16>(vx, c.v + to, scale(1, h));
     };
 #pragma unroll
     for (int a = 0; a < kAhead; a++)
