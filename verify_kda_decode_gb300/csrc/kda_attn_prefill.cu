@@ -42,11 +42,9 @@ namespace {
 constexpr int kHalf = 128, kRowsCta = 256, kKeys = 128;
 constexpr int kSoftmax = 256, kLoaders = 128, kThreads = kSoftmax + kLoaders + 128;
 // Registers of a thread: all start with 128 (512 threads, the whole file), then the softmax holds a row
-// of S at once, the loaders two fetches of E4M3 codes; 256 x 184 + 128 x 80 + 128 x 64 = 65536.
+// of S at once; 256 x 184 + 128 x 80 + 128 x 64 = 65536.
 constexpr int kRegs = 128, kRegsMma = 64;
-template <bool FP8> constexpr int kRegsSoftmax = FP8 ? 176 : 184;
-template <bool FP8> constexpr int kRegsLoad = FP8 ? 96 : 80;
-constexpr uint32_t kSlots = 4;
+constexpr int kRegsSoftmax = 184, kRegsLoad = 80;
 constexpr int kHalfBytes = kKeys * 128;   // a tile's 64 head dims: 128 rows of 128 bytes
 constexpr int kMaxSplitCtas = 256;             // CTAs of a launch, and pieces of split units
 constexpr int kMaxSplits = 32;                 // pieces of a unit (their join reads one after the other)
@@ -66,10 +64,14 @@ struct Unit {
     int slot, first, group;   // ... this piece's and the first one's place in the workspace, the split unit's number
 };
 
-template <int D>
+// A ring of four tiles; with an E4M3 cache three, and three fetches of codes on their way to it.
+template <int D, bool FP8>
 struct Smem {
+    static constexpr uint32_t kSlots = FP8 ? 3 : 4;
+    static constexpr int kRaw = 3;
     uint8_t q[2][kHalf * D * 2];
     uint8_t kv[kSlots][kKeys * D * 2];
+    uint8_t raw[FP8 ? kRaw : 1][FP8 ? kKeys * D : 16];
     uint64_t q_full[2], q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
     Unit unit[kUnits];
     int before[kTable + 1], warp_sum[16];   // row tiles of the sequences before each one
@@ -127,8 +129,7 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-static_assert(kSoftmax * kRegsSoftmax<false> + kLoaders * kRegsLoad<false> + 128 * kRegsMma <= kThreads * kRegs &&
-              kSoftmax * kRegsSoftmax<true> + kLoaders * kRegsLoad<true> + 128 * kRegsMma <= kThreads * kRegs, "setmaxnreg would wait forever");
+static_assert(kSoftmax * kRegsSoftmax + kLoaders * kRegsLoad + 128 * kRegsMma <= kThreads * kRegs, "setmaxnreg would wait forever");
 
 __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1)
 {
@@ -211,8 +212,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, 
 }
 
 // Bounded wait: after two seconds, or when another role has given up, the CTA winds down.
-template <int D>
-__device__ __forceinline__ bool wait_long(Smem<D> &sm, uint64_t *bar, uint32_t parity, int *err)
+template <typename SM>
+__device__ __forceinline__ bool wait_long(SM &sm, uint64_t *bar, uint32_t parity, int *err)
 {
     const uint64_t t0 = globaltimer_ns();
     while (!sm.stop) {
@@ -226,8 +227,8 @@ __device__ __forceinline__ bool wait_long(Smem<D> &sm, uint64_t *bar, uint32_t p
     return false;
 }
 // ... by all lanes of a warp, which agree on the outcome
-template <int D>
-__device__ __forceinline__ bool wait_warp(Smem<D> &sm, uint64_t *bar, uint32_t parity, int *err)
+template <typename SM>
+__device__ __forceinline__ bool wait_warp(SM &sm, uint64_t *bar, uint32_t parity, int *err)
 {
     for (int i = 0; i < 64; i++)   // the usual wait ends here, without a look at the clock
         if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
@@ -235,16 +236,16 @@ __device__ __forceinline__ bool wait_warp(Smem<D> &sm, uint64_t *bar, uint32_t p
 }
 
 // A role's k-th unit, left by warp 13 in shared memory: null when there is no more (or a wait gave up).
-template <int D>
-__device__ __forceinline__ const Unit *unit_of(Smem<D> &sm, int k, int *err)
+template <typename SM>
+__device__ __forceinline__ const Unit *unit_of(SM &sm, int k, int *err)
 {
     if (!wait_warp(sm, &sm.u_full[k % kUnits], (k / kUnits) & 1, err)) return nullptr;
     const Unit *u = &sm.unit[k % kUnits];
     return u->idx >= 0 ? u : nullptr;
 }
 // ... and that this warp is done with it.
-template <int D>
-__device__ __forceinline__ void unit_done(Smem<D> &sm, int k)
+template <typename SM>
+__device__ __forceinline__ void unit_done(SM &sm, int k)
 {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.u_empty[k % kUnits]);
@@ -263,12 +264,12 @@ __device__ __forceinline__ bool elect_one()
 // run in order).  The whole warp walks the loop, so that the descriptors stay in uniform registers, and
 // one lane issues.
 // `item`: ring items so far; `tiles`: key tiles so far of each half; `units`: units with products so far
-template <int D, typename Q, int HALVES>
-__device__ __forceinline__ bool issue_products(Smem<D> &sm, int n, uint32_t tmem, uint32_t &item, uint32_t *tiles, uint32_t &units, int *err)
+template <int D, typename Q, int HALVES, typename SM>
+__device__ __forceinline__ bool issue_products(SM &sm, int n, uint32_t tmem, uint32_t &item, uint32_t *tiles, uint32_t &units, int *err)
 {
     const uint64_t q_desc = desc_sw128(smem_u32(sm.q[0]), 16u), k_desc = desc_sw128(smem_u32(sm.kv[0]), 16u),
                    v_desc = desc_sw128(smem_u32(sm.kv[0]), kHalfBytes);
-    constexpr uint32_t kTile = kKeys * D * 2 >> 4;   // a ring slot, a half's queries, in descriptor units
+    constexpr uint32_t kSlots = SM::kSlots, kTile = kKeys * D * 2 >> 4;   // a ring slot, a half's queries, in descriptor units
     auto slot_wait = [&](uint32_t it) { return wait_warp(sm, &sm.full[it % kSlots], (it / kSlots) & 1, err); };
     auto qk = [&](int h, uint32_t it, bool last_tile) {
         const uint64_t ad = q_desc + h * kTile, bd = k_desc + (it % kSlots) * kTile;
@@ -317,8 +318,8 @@ __device__ __forceinline__ bool issue_products(Smem<D> &sm, int n, uint32_t tmem
     return true;
 }
 
-template <int D, typename Q>
-__device__ void mma_role(Smem<D> &sm, uint32_t tmem, int *err)
+template <int D, typename Q, typename SM>
+__device__ void mma_role(SM &sm, uint32_t tmem, int *err)
 {
     uint32_t item = 0, tiles[2] = {0, 0}, units = 0;
     for (int k = 0; const Unit *u = unit_of(sm, k, err); k++) {
@@ -345,9 +346,10 @@ __device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, 
 // ---- warps 8-11: a unit's queries, then keys and values of tile i as ring items 2 i and 2 i + 1
 // (`item`: ring items so far, `units`: units so far)
 template <int D, typename Q, bool FP8>
-__device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, int S, uint32_t &item, uint32_t &units)
+__device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int W, int S, uint32_t &item, uint32_t &units)
 {
     const AttnParams &p = args.p;
+    constexpr uint32_t kSlots = Smem<D, FP8>::kSlots;
     const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
     const PagedCache &c = p.c;
     const int tid = threadIdx.x - kSoftmax, w = tid >> 5, lane = tid & 31, r8 = lane & 7, q4 = lane >> 3;
@@ -482,37 +484,43 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
     } else {
         if (!load_queries()) return false;
         queries_done();
-        // codes pass through registers: the next item's loads are in flight while this one's are
-        // converted (exactly) to halves and stored
-        uint4 cur[GR * PASS > 0 ? GR * PASS : 1], nxt[GR * PASS > 0 ? GR * PASS : 1];
-        auto fetch = [&](int it, uint4 *v, int pg_lane) {
-            const uint8_t *base = it & 1 ? c.v : c.k;
+        // Codes come to shared memory three items ahead (each thread's own pieces, so that only its own copies are
+        // waited for) and are converted (exactly) to halves on their way into the ring.  With one item ahead,
+        // in registers, a tile pair took 3.0 us; like this 2.5 us (16-bit caches: 1.54).
+        constexpr int kRaw = Smem<D, FP8>::kRaw;
+        int sent = 0;   // items whose copies are under way
+        auto send = [&]() {
+            if (sent < 2 * n) {
+                const uint8_t *base = sent & 1 ? c.v : c.k;
+                uint8_t *dst = sm.raw[sent % kRaw] + tid * 16;
 #pragma unroll
-            for (int a = 0; a < GR; a++) {
-                const int gi = w + 4 * a;
-                const uint8_t *src = source(base, it >> 1, gi, __shfl_sync(~0u, pg_lane, gi));
+                for (int a = 0; a < GR; a++) {
+                    const int gi = w + 4 * a;
+                    const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi));
 #pragma unroll
-                for (int x = 0; x < PASS; x++)
-                    v[a * PASS + x] = src ? __ldg(reinterpret_cast<const uint4 *>(src + (x * 4 + q4) * 16)) : make_uint4(0, 0, 0, 0);
+                    for (int x = 0; x < PASS; x++)
+                        cp_async16(dst + (a * PASS + x) * (kLoaders * 16), src ? src + (x * 4 + q4) * 16 : c.k, src ? 16 : 0);
+                }
+                if (sent & 1) {
+                    pages = pages_next;
+                    pages_next = pages_of((sent >> 1) + 2);
+                }
             }
+            sent++;
+            cp_async_commit();
         };
-        fetch(0, cur, pages);
+        for (int i = 0; i < kRaw; i++) send();
         for (int it = 0; it < 2 * n; it++) {
             const uint32_t ring = item + it;
             const int slot = ring % kSlots;
-            if (it + 1 < 2 * n) {
-                if (it & 1) {
-                    pages = pages_next;
-                    pages_next = pages_of((it >> 1) + 2);
-                }
-                fetch(it + 1, nxt, pages);
-            }
+            cp_async_wait<kRaw - 1>();
             if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
+            const uint4 *src = reinterpret_cast<const uint4 *>(sm.raw[it % kRaw]) + tid;
 #pragma unroll
             for (int a = 0; a < GR; a++)
 #pragma unroll
                 for (int x = 0; x < PASS; x++) {
-                    const uint4 v = cur[a * PASS + x];
+                    const uint4 v = src[(a * PASS + x) * kLoaders];
                     const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
                     uint32_t e[8];
 #pragma unroll
@@ -524,9 +532,9 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
                 }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.full[slot]);
-#pragma unroll
-            for (int a = 0; a < GR * PASS; a++) cur[a] = nxt[a];
+            send();
         }
+        cp_async_wait<0>();
     }
     item += 2 * n;
     units++;
@@ -534,14 +542,16 @@ __device__ bool load_unit(Smem<D> &sm, const Args &args, const Unit &u, int W, i
 }
 
 template <int D, typename Q, bool FP8>
-__device__ void load_role(Smem<D> &sm, const Args &args, int W, int S)
+__device__ void load_role(Smem<D, FP8> &sm, const Args &args, int W, int S)
 {
+    constexpr uint32_t kSlots = Smem<D, FP8>::kSlots;
     uint32_t item = 0, units = 0;
     for (int k = 0; const Unit *at = unit_of(sm, k, args.p.c.err); k++) {
         const Unit u = *at;
         unit_done(sm, k);
         if (u.tb > u.ta && !load_unit<D, Q, FP8>(sm, args, u, W, S, item, units)) break;
     }
+    cp_async_wait<0>();
     // where a wait gave up, tiles may still be landing: let them (the last one of each slot)
     if (sm.stop)
         for (uint32_t i = item < kSlots ? 0 : item - kSlots; i < item + kSlots; i++)
@@ -604,7 +614,7 @@ __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const 
 // ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far; `all_units`:
 // those of either half)
 template <int D, typename Q, bool FP8>
-__device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
+__device__ bool softmax_unit(Smem<D, FP8> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
                              uint32_t &tiles, uint32_t &units, uint32_t all_units)
 {
     const PagedCache &c = p.c;
@@ -721,8 +731,8 @@ __device__ bool softmax_unit(Smem<D> &sm, const AttnParams &p, const Unit &u, ui
 }
 
 // Meeting point of the eight softmax warps, bounded like every wait.
-template <int D>
-__device__ __forceinline__ bool softmax_sync(Smem<D> &sm, uint32_t &joins, int *err)
+template <typename SM>
+__device__ __forceinline__ bool softmax_sync(SM &sm, uint32_t &joins, int *err)
 {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.join);
@@ -730,7 +740,7 @@ __device__ __forceinline__ bool softmax_sync(Smem<D> &sm, uint32_t &joins, int *
 }
 
 template <int D, typename Q, bool FP8>
-__device__ void softmax_role(Smem<D> &sm, const AttnParams &p, uint32_t tmem, int W, int S)
+__device__ void softmax_role(Smem<D, FP8> &sm, const AttnParams &p, uint32_t tmem, int W, int S)
 {
     const int tid = threadIdx.x, h = tid >> 7;
     int *count = reinterpret_cast<int *>(p.ws);
@@ -787,8 +797,8 @@ __device__ __forceinline__ SeqInfo prefill_seq(const AttnParams &p, int b, int &
 }
 
 // ---- warp 13: units in order of their number, handed to the other roles a few ahead
-template <int D>
-__device__ void unit_role(Smem<D> &sm, const AttnParams &p, int W, int S)
+template <typename SM>
+__device__ void unit_role(SM &sm, const AttnParams &p, int W, int S)
 {
     const PagedCache &c = p.c;
     const int lane = threadIdx.x & 31;
@@ -897,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // the swizzle repeats every 1024 bytes of the shared address
-    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    Smem<D, FP8> &sm = *reinterpret_cast<Smem<D, FP8> *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const AttnParams &p = args.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
@@ -906,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.join, kSoftmax / 32);
         mbar_init(&sm.drain, 1);
-        for (int i = 0; i < (int)kSlots; i++) {
+        for (int i = 0; i < (int)Smem<D, FP8>::kSlots; i++) {
             mbar_init(&sm.full[i], kLoaders);
             mbar_init(&sm.empty[i], 1);
         }
@@ -957,19 +967,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
     }
     const uint32_t tmem = sm.tmem;
     if (warp < 8) {
-        regs_inc<kRegsSoftmax<FP8>>();
+        regs_inc<kRegsSoftmax>();
         softmax_role<D, Q, FP8>(sm, p, tmem, W, S);
         __syncwarp();
         regs_dec<kRegs>();   // back to what the common code was compiled for
     } else if (warp < 12) {
-        regs_dec<kRegsLoad<FP8>>();
+        regs_dec<kRegsLoad>();
         load_role<D, Q, FP8>(sm, args, W, S);
         __syncwarp();
         regs_inc<kRegs>();
     } else {
         regs_dec<kRegsMma>();
         if (warp == 12) mma_role<D, std::conditional_t<FP8, Half, Q>>(sm, __reduce_max_sync(~0u, tmem), p.c.err);
-        else if (warp == 13) unit_role<D>(sm, p, W, S);
+        else if (warp == 13) unit_role(sm, p, W, S);
         __syncwarp();
         regs_inc<kRegs>();
     }
@@ -1035,7 +1045,7 @@ template <int D, typename Q, bool FP8>
 cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr size_t smem = sizeof(Smem<D>) + 1024;
+    constexpr size_t smem = sizeof(Smem<D, FP8>) + 1024;
     cudaError_t e = setup.get(kda_attn_prefill_kernel<D, Q, FP8>, kThreads, smem, 0, nullptr);
     if (e != cudaSuccess) return e;
     int sms = 0;
