@@ -47,6 +47,7 @@ constexpr int kRegs = 128, kRegsMma = 64;
 constexpr int kRegsSoftmax = 184, kRegsLoad = 80;
 constexpr int kHalfBytes = kKeys * 128;   // a tile's 64 head dims: 128 rows of 128 bytes
 constexpr int kMaxSplitCtas = 256;             // CTAs of a launch, and pieces of split units
+constexpr int kMinShare = 8;                   // key tiles of a piece at least
 constexpr int kMaxSplits = 32;                 // pieces of a unit (their join reads one after the other)
 constexpr uint64_t kLimitNs = 2000000000ull;   // bound of every wait
 constexpr int kUnits = 2, kTable = 512;         // units on their way to the roles; sequences whose tile counts are kept on chip
@@ -874,8 +875,12 @@ __device__ void unit_role(SM &sm, const AttnParams &p, int W, int S)
             u.p_first = u.len - u.n + u.t0;
             u.p_last = u.len - u.n + (u.r0 + u.rows - 1) / p.G;
             const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
-            // this split's share of the key tiles, two at least; splits past the last piece have none
-            const int share = splits > 1 ? max(2, (kr.count + splits - 1) / splits) : max(1, kr.count);
+            // This split's share of the key tiles; splits past the last piece have none.  A tile takes 1.5 us, and one
+            // CTA joins the pieces at about 3 us each, so their best number grows with the root of the tiles
+            // (64 tokens behind 4096, 8 key heads: 59 us in 16 pieces, 35 in 4; behind 16384: 78 us in 19, 60 in 8;
+            // behind 1000, 8 tiles: 26 us in 4, 21 in one).
+            int share = max(1, kr.count);
+            if (splits > 1) share = max(kMinShare, max((kr.count + splits - 1) / splits, (int)ceilf(sqrtf(2.f * kr.count))));
             u.pieces = max(1, (kr.count + share - 1) / share);
             u.ta = min(kr.count, y * share);
             u.tb = min(kr.count, u.ta + share);
