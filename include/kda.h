@@ -380,7 +380,9 @@ kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t
  *   lse = m + log(sum_j exp(s_j - m)).  A token that sees no key (a row shorter than the call's
  *   tokens puts its first ones at negative positions) gets out = 0, lse = -inf.
  * Query head h reads kv head h / (num_q_heads / num_kv_heads).  Keys that no token of the call
- * sees are not read (their table entries may be -1, their contents anything).  Products are
+ * sees are not read (their table entries may be -1, their contents anything); the value of
+ * a key that is hidden from one token and seen by another of its sequence and call counts 0 times
+ * for the first, so a NaN or an infinity in it can reach both.  Products are
  * taken in the query's type (a 16-bit cache must have it too; E4M3 codes are exact in both) with
  * FP32 sums; the softmax statistics are FP32.
  * Workspace: kda_attn_workspace_size() bytes, 256-byte aligned, ZEROED by the caller once; every

@@ -205,3 +205,18 @@ def test_binding_checks_tensors(K):
         K.kda_kv_append(c, 0, rows, k[None], k[None], cu_seqlens=torch.zeros(2, dtype=i32))
     with pytest.raises(TypeError):
         K.kda_kv_extend(c, rows, torch.zeros(1))
+
+
+def test_binding_refuses_numbers_past_32_bits(K):
+    """2^32 + 1 does not arrive as 1."""
+    c, i32, past = cpu_cache(K), torch.int32, (1 << 32) + 1
+    rows, cu = torch.zeros(1, dtype=i32), torch.zeros(2, dtype=i32)
+    q, k = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
+    many = k[0, :1].expand(past, 2, 64)   # no memory behind it
+    for call in (lambda: K.kda_kv_extend(c, rows, past), lambda: K.kda_kv_append(c, past, rows, k, k),
+                 lambda: K.kda_kv_append(c, 0, rows, many, many, cu_seqlens=cu),
+                 lambda: K.kda_attn_decode(c, past, rows, q), lambda: K.kda_attn_decode(c, 0, rows, q, window=past),
+                 lambda: K.kda_attn_decode(c, 0, rows, q, window=4, sinks=past),
+                 lambda: K.kda_attn_prefill(c, past, rows, cu, 1, q[0]), lambda: K.kda_attn_prefill(c, 0, rows, cu, past, q[0])):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()

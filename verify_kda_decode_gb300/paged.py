@@ -159,6 +159,14 @@ def kda_attn_workspace_size(cache: KdaKvCache) -> int:
     return int(_lib.kda_attn_workspace_size(ctypes.byref(cache.c_struct())))
 
 
+def _i32(x, name: str) -> int:
+    """x as a C int32 (ctypes would cut higher bits off in silence)."""
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{name}={x} does not fit 32 bits")
+    return x
+
+
 def _ints(t: torch.Tensor, name: str, n: int, dev) -> int:
     _need(t, name, torch.int32, (n,), dev)
     return t.data_ptr()
@@ -178,7 +186,7 @@ def kda_kv_extend(cache: KdaKvCache, rows, n_tokens: Union[int, torch.Tensor], w
     distinct), once per step for all layers; a partly filled last page that others share is copied."""
     _, st, _, dev = cache._struct()
     pr, B = _rows(rows, dev)
-    pn, n = (None, int(n_tokens)) if not isinstance(n_tokens, torch.Tensor) else (_ints(n_tokens, "n_tokens", B, dev), 0)
+    pn, n = (None, _i32(n_tokens, "n_tokens")) if not isinstance(n_tokens, torch.Tensor) else (_ints(n_tokens, "n_tokens", B, dev), 0)
     ws, nb = cache._workspace("_kv_ws", workspace)
     _call(dev, _lib.kda_kv_extend, st, pr, pn, n, B, ws, nb, _stream(stream, dev))
 
@@ -223,6 +231,7 @@ def _tokens(t: torch.Tensor, name: str, packed: bool, heads: Optional[int], cach
                          f"{'Hq' if heads is None else heads}, {D}]")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    _i32(max(n), f"{name}: size")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
@@ -277,7 +286,7 @@ def kda_kv_append(cache: KdaKvCache, layer: int, rows, k, v, cu_seqlens=None, n_
     T, kl, vl = _plan(cache, ("append", B, cu_seqlens is None, k.dtype, v.dtype, k.device, v.device, k.shape, v.shape, k.stride(), v.stride()), make)
     pc = None if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", B + 1, dev)
     pn = None if n_tokens is None else _ints(n_tokens, "n_tokens", B, dev)
-    _call(dev, _lib.kda_kv_append, st, layer, pr, B, T, pn, pc, k.data_ptr(), kl, v.data_ptr(), vl, _stream(stream, dev))
+    _call(dev, _lib.kda_kv_append, st, _i32(layer, "layer"), pr, B, T, pn, pc, k.data_ptr(), kl, v.data_ptr(), vl, _stream(stream, dev))
 
 
 def _attn(cache: KdaKvCache, q, packed: bool, scale, window, sinks, out, lse, return_lse):
@@ -289,7 +298,7 @@ def _attn(cache: KdaKvCache, q, packed: bool, scale, window, sinks, out, lse, re
     def make():
         ql = _tokens(q, "q", packed, None, cache)
         D = cache.head_dim
-        desc = _Desc(shape[-2], 1.0 / math.sqrt(D) if scale is None else float(scale), int(window), int(sinks), ql)
+        desc = _Desc(shape[-2], 1.0 / math.sqrt(D) if scale is None else float(scale), _i32(window, "window"), _i32(sinks, "sinks"), ql)
         return ctypes.byref(desc), shape[:-1]
 
     desc, rows_shape = _plan(cache, ("attn", packed, scale, window, sinks, q.dtype, q.device, shape, q.stride()), make)
@@ -318,7 +327,7 @@ def kda_attn_decode(cache: KdaKvCache, layer: int, rows, q, scale: Optional[floa
         raise ValueError(f"q: {q.shape[0]} sequences, rows has {B}")
     pn = None if n_tokens is None else _ints(n_tokens, "n_tokens", B, dev)
     ws, nb = cache._workspace("_attn_ws", workspace)
-    _call(dev, _lib.kda_attn_decode, st, layer, desc, pr, B, q.shape[1], pn, q.data_ptr(), out.data_ptr(), _ptr(lse), ws, nb,
+    _call(dev, _lib.kda_attn_decode, st, _i32(layer, "layer"), desc, pr, B, q.shape[1], pn, q.data_ptr(), out.data_ptr(), _ptr(lse), ws, nb,
           _stream(stream, dev))
     return out if lse is None else (out, lse)
 
@@ -334,7 +343,7 @@ def kda_attn_prefill(cache: KdaKvCache, layer: int, rows, cu_seqlens, max_len: i
     desc, out, lse = _attn(cache, q, True, scale, window, sinks, out, lse, return_lse)
     pc = _ints(cu_seqlens, "cu_seqlens", B + 1, dev)
     ws, nb = cache._workspace("_attn_ws", workspace)
-    _call(dev, _lib.kda_attn_prefill, st, layer, desc, pr, B, pc, q.shape[0], int(max_len), q.data_ptr(), out.data_ptr(), _ptr(lse),
+    _call(dev, _lib.kda_attn_prefill, st, _i32(layer, "layer"), desc, pr, B, pc, q.shape[0], _i32(max_len, "max_len"), q.data_ptr(), out.data_ptr(), _ptr(lse),
           ws, nb, _stream(stream, dev))
     return out if lse is None else (out, lse)
 
