@@ -37,6 +37,12 @@ constexpr int kUnitRows = 32;
 // sequences, four drafts, 1024 window: 70 us, with 2 / 4 / 8: 47 / 41 / 41 us; 131072 tokens of one
 // sequence: 91 us, 90 / 89 / 94 us.
 constexpr int kUnitCost = 4;
+// How many places longer a run may get for whole units to each CTA (see where the runs are made).  64 ragged
+// sequences in a 1024 window, 20 rows a unit: 35.3 us with cut units, 31.1 with whole ones (9 places more); 32 of 1024
+// tokens 21.0 and 17.5 us (12 more); 64 of 1024 tokens, 128 dims, two units a CTA: 50.4 and 53.1 us (18 more); 40
+// of 4096: 61 and 67 us (32 more).  One sequence, 8 key heads: of 300 tokens 9.3 and 7.5 us (8 more), of 517 tokens
+// 8.3 and 9.9 us (12 more).
+constexpr int kUneven = 12, kUnevenShort = 8;
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
     constexpr int ROWS = 8 * NB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long sh_prefix, sh_warp[kWarps];
-    __shared__ int sh_b, sh_last, sh_seq[3][kSeqs];
+    __shared__ int sh_b, sh_last, sh_units[kWarps], sh_most[kWarps], sh_seq[3][kSeqs];
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, cc = lane & 3;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
@@ -153,22 +159,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
 
     // ---- this CTA's run of tiles
     auto load_seq = [&](int b, bool report) { return seq_info(c, p.rows[b], p.n_tokens ? p.n_tokens[b] : p.T, p.T, report); };
+    int place = 0;   // places of a unit on the line of work: kUnitCost, then one for each of its tiles, or (not 0) this many
     auto tiles_of = [&](const SeqInfo &s, int &kt, int &mt) -> long long {   // kt tiles in each of Hkv * mt units
-        // (the line of work gives each unit kUnitCost places, then one for each of its tiles)
         kt = mt = 0;
         if (!s.ok || s.n == 0) return 0;
         const KeyRange<kTileKeys> r(s.len - s.n, s.len - 1, s.len, W, S);
         kt = max(1, r.count);
         mt = (s.n * p.G + ROWS - 1) / ROWS;
-        return (long long)(kt + kUnitCost) * mt * c.Hkv;
+        return (long long)(place ? place : kt + kUnitCost) * mt * c.Hkv;
     };
     const int per = (p.B + kThreads - 1) / kThreads, b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
     long long mine = 0;
-    int kt, mt;
+    int kt, mt, units = 0, most = 0;   // (units: 2^20 at most)
     for (int b = b_lo; b < b_hi; b++) {
         const SeqInfo s = load_seq(b, blockIdx.x == 0);
         if (b < kSeqs) sh_seq[0][b] = s.row, sh_seq[1][b] = s.len, sh_seq[2][b] = s.ok ? s.n : 0;
         mine += tiles_of(s, kt, mt);
+        units = min(units + mt * c.Hkv, 1 << 20);
+        if (mt) most = max(most, kt + kUnitCost);
     }
     auto seq_of = [&](int b) {   // after the barrier below
         if (b >= kSeqs) return load_seq(b, false);
@@ -177,21 +185,47 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         return s;
     };
     long long before = mine;
+    const int warp_units = __reduce_add_sync(~0u, units);
+    most = __reduce_max_sync(~0u, most);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(~0u, before, o);
         if (lane >= o) before += y;
     }
-    if (lane == 31) sh_warp[w] = before;
+    if (lane == 31) sh_warp[w] = before, sh_units[w] = warp_units, sh_most[w] = most;
     __syncthreads();
     before -= mine;
     long long total = 0;
+    int all_units = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; i++) {
         if (i < w) before += sh_warp[i];
         total += sh_warp[i];
+        all_units += sh_units[i];
+        most = max(most, sh_most[i]);
     }
-    const long long chunk = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
+    long long chunk = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
+    // Whole units to each CTA, places as many as the longest unit has, where the longest run gets no more than kUneven
+    // places longer (kUnevenShort, where the runs are shorter than a unit's start): no unit is started twice and none
+    // is joined.
+    const int each = all_units <= (int)gridDim.x ? 1 : (all_units + gridDim.x - 1) / gridDim.x;
+    if (all_units < 1 << 20 && (long long)each * most <= chunk + (chunk > kUnitCost ? kUneven : kUnevenShort)) {
+        int x = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        x -= units;
+#pragma unroll
+        for (int i = 0; i < kWarps; i++)
+            if (i < w) x += sh_units[i];
+        place = most;
+        mine = (long long)units * most;
+        before = (long long)x * most;
+        total = (long long)all_units * most;
+        chunk = max(1ll, (long long)each * most);
+    }
     const long long begin = blockIdx.x * chunk, end = min(total, begin + chunk);
     if (begin >= end) return;
     if (begin >= before && begin < before + mine) {
@@ -226,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             seq = seq_of(++b);
             seq_tiles = tiles_of(seq, kt, mt);
         }
-        const int local = (int)div_pos(at - prefix, kt + kUnitCost);
+        const int unit = place ? place : kt + kUnitCost, local = (int)div_pos(at - prefix, unit);
         const int h = local / mt, mb = local % mt;
-        const long long u0 = prefix + (long long)local * (kt + kUnitCost) + kUnitCost;   // the unit's tiles: places [u0, u0 + kt)
+        const long long u0 = prefix + (long long)local * unit + unit - kt;   // the unit's tiles: places [u0, u0 + kt)
         if (u0 >= end) break;   // they belong to the next CTAs
         const int ta = (int)(max(at, u0) - u0), tb = (int)min((long long)kt, end - u0);
         const int n_rows = min(ROWS, seq.n * p.G - mb * ROWS);
