@@ -94,6 +94,15 @@ def test_decode_more_sequences_than_are_kept_on_chip(K):
     run_decode(K, lens, 1, 1, 2, 64, 16, BF, BF, seed=5)
 
 
+@pytest.mark.parametrize("T,G", [(1, 2), (4, 5), (16, 4)])
+def test_decode_whole_units_and_cut_ones(K, T, G):
+    """Runs of whole units (one or several a CTA, rows without tokens between them) and runs that cut them."""
+    none = lambda B: [0 if i % 5 == 2 else T for i in range(B)]
+    for lens in ([T + (11 * i) % 50 for i in range(90)], [T + 1000 - (i % 60) for i in range(40)], [T + 600] * 30 + [3000]):
+        run_decode(K, lens, T, 8, G, 64, 16, FH, FH, seed=T, n_tokens=none(len(lens)))
+    run_decode(K, [T + (7 * i) % 300 for i in range(280)], T, 2, G, 64, 16, BF, BF, 100, 3, seed=9, n_tokens=none(280))
+
+
 def test_decode_layers_scale_and_extreme_scores(K):
     run_decode(K, [33, 100], 1, 2, 4, 64, 16, BF, BF, layers=3, layer=2, scale=0.0, seed=6)
     run_decode(K, [33, 100], 2, 2, 4, 128, 16, BF, BF, layers=3, layer=1, scale=3.0, seed=7)   # near one-hot rows
