@@ -1,9 +1,10 @@
 """ctypes binding of libkda's paged key-value cache and the attention that reads it (include/kda.h).
 
 Argument checks and marshalling only, in the manner of ``kda.py``: tensors are torch CUDA tensors,
-calls run on the current stream of the cache's device with that device current.  A cache's
-workspaces are made on first use and belong to it: calls on one cache that may overlap on the
-GPU (two streams without an order between them) have to pass workspaces of their own.
+calls run on the current stream of the cache's device with that device current.  A cache's own
+workspaces are made and cleared with it, before its constructor returns: its calls may run on any
+stream and be captured from the first one on.  Calls on one cache that may overlap on the GPU (two
+streams without an order between them) have to pass workspaces of their own.
 """
 from __future__ import annotations
 
@@ -55,6 +56,7 @@ class KdaKvCache:
     def __post_init__(self):
         if self.err_word is None:
             self.err_word = torch.zeros(1, dtype=torch.int32, device=self.k.device)
+        self._make_workspaces()
 
     @staticmethod
     def zeros(layers: int, num_pages: int, Hkv: int, rows: int, max_pages: int, page_size: int = 64,
@@ -88,11 +90,11 @@ class KdaKvCache:
         return self.k.shape[1]
 
     def __setattr__(self, name, value):
-        # another tensor in a field: the struct, the workspaces and what was checked against it go
+        # another tensor in a field: the struct and what was checked against it go
         d = self.__dict__
         d[name] = value
         if not name.startswith("_"):
-            for k in ("_c_struct", "_kv_ws", "_attn_ws", "_plans"):
+            for k in ("_c_struct", "_plans"):
                 d.pop(k, None)
 
     def c_struct(self) -> _Cache:
@@ -131,24 +133,56 @@ class KdaKvCache:
         st = _Cache(_ptr(self.k), _ptr(self.v), _TYPES[self.k.dtype], layers, pages, Hkv, ps, D, rows, width,
                     _ptr(self.page_table), _ptr(self.seq_lens), _ptr(self.page_refs),
                     _ptr(self.k_scale) if fp8 else None, _ptr(self.v_scale) if fp8 else None, _ptr(self.err_word))
-        for k in ("_kv_ws", "_attn_ws", "_plans"):
-            d.pop(k, None)
+        d.pop("_plans", None)
         d["_c_struct"] = cached = (st, ctypes.byref(st), ptrs, dev)
+        self._make_workspaces()
         return cached
 
+    def _make_workspaces(self):
+        """Makes and clears the cache's own workspaces, where there are none that fit its tensors.  The clear
+        (and that of an error word made here) has run when this returns, so that no stream needs an order
+        with it.  Inside a capture it would only run with the graph: none is made there."""
+        d, dev = self.__dict__, self.k.device
+        if self.k.dim() != 5 or self.page_table.dim() != 2:
+            return
+        capturing = _capturing(dev)
+        st = _Cache(num_pages=self.k.shape[1], head_dim=self.k.shape[4], rows=self.page_table.shape[0])
+        made = False
+        for kind, size in (("_kv_ws", _lib.kda_kv_workspace_size), ("_attn_ws", _lib.kda_attn_workspace_size)):
+            n, old = max(256, int(size(ctypes.byref(st)))), d.get(kind)
+            if old is not None and old.numel() >= n and old.device == dev:
+                continue
+            if capturing:
+                d[kind] = None
+            else:
+                if old is not None and old.is_cuda:
+                    torch.cuda.synchronize(old.device)   # calls on any stream may still use it
+                d[kind] = torch.zeros(n, dtype=torch.uint8, device=dev)
+                made = True
+        if made and dev.type == "cuda":
+            torch.cuda.current_stream(dev).synchronize()
+
     def _workspace(self, kind: str, given: Optional[torch.Tensor]) -> Tuple[int, int]:
-        """(pointer, bytes) of the given workspace, or of the cache's own (zeroed when made)."""
+        """(pointer, bytes) of the given workspace, or of the cache's own."""
         if given is not None:
             if given.device != self.device or not given.is_contiguous():
                 raise ValueError("workspace must be a contiguous tensor on the cache's device")
             return given.data_ptr(), given.numel() * given.element_size()
         own = self.__dict__.get(kind)
         if own is None:
-            size = _lib.kda_kv_workspace_size if kind == "_kv_ws" else _lib.kda_attn_workspace_size
-            t = torch.zeros(max(256, int(size(self._struct()[1]))), dtype=torch.uint8, device=self.device)
-            own = (t.data_ptr(), t.numel(), t)
-            self.__dict__[kind] = own
-        return own[0], own[1]
+            self._make_workspaces()
+            own = self.__dict__.get(kind)
+            if own is None:
+                raise RuntimeError("no workspace can be made while a graph is captured: make the cache before the capture, or pass workspace=")
+        return own.data_ptr(), own.numel()
+
+
+def _capturing(dev: torch.device) -> bool:
+    """Whether the current stream of this device is being captured into a graph."""
+    if dev.type != "cuda":
+        return False
+    with torch.cuda.device(dev):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def kda_kv_workspace_size(cache: KdaKvCache) -> int:
