@@ -30,7 +30,9 @@
 // seen by some token of the CTA comes by TMA, one box for each page and half; at the ends of the range
 // the loader threads copy it themselves and write zeros for the keys that no token sees, so that
 // whatever the page holds there (NaN included) cannot reach the products.  The same threads convert E4M3
-// codes on their way.
+// codes on their way.  Keys that are seen but whose table entry names no page come as zeros too, and the loaders
+// leave the softmax a word for each tile that says which groups of 8 keys these are (4 x 4096 tokens 395.2 -> 397.7 us; with
+// the pages looked up beside the sums 402 to 414).
 #include <cuda.h>
 
 #include "kda_attn_common.cuh"
@@ -51,6 +53,7 @@ constexpr int kMinShare = 8;                   // key tiles of a piece at least
 constexpr int kMaxSplits = 32;                 // pieces of a unit (their join reads one after the other)
 constexpr uint64_t kLimitNs = 2000000000ull;   // bound of every wait
 constexpr int kUnits = 2, kTable = 512;         // units on their way to the roles; sequences whose tile counts are kept on chip
+constexpr int kGone = 8;                       // tiles whose missing pages are told to the softmax (four would do, see load_unit)
 constexpr float kGrow = 8.f;                   // log2 growth of the maximum that O is rescaled for
 
 // What a CTA works on: rows [r0, r0 + rows) of the n * G of a sequence, and key tiles [ta, tb) of their range.
@@ -74,6 +77,7 @@ struct Smem {
     uint8_t kv[kSlots][kKeys * D * 2];
     uint8_t raw[FP8 ? kRaw : 1][FP8 ? kKeys * D : 16];
     uint64_t q_full[2], q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
+    unsigned gone[kGone];                   // by the tile's number: groups of 8 keys that are seen but have no page
     Unit unit[kUnits];
     int before[kTable + 1], warp_sum[16];   // row tiles of the sequences before each one
     int4 seq[kTable];                       // row, length, new tokens, first packed token
@@ -360,13 +364,22 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
     constexpr int PASS = CPR / 4;             // passes of four chunks over a group of 8 keys
     constexpr int GR = kKeys / 8 / 4;         // groups of 8 keys of a warp: w, w + 4, ...
     const size_t head_bytes = (size_t)c.ps * RB;
-    // page of key group `lane` (16 groups of a tile), -1: none of its keys is seen
+    // page of key group `lane` (16 groups of a tile), 0 where none of its keys is seen (and no page is looked at)
     auto pages_of = [&](int i) {
         const int k0 = kr.tile(u.ta + i) * kKeys + lane * 8;
-        if (i >= n || lane >= kKeys / 8 || k0 >= kr.end || !(k0 + 8 > kr.lo || k0 < S)) return -1;
+        if (i >= n || lane >= kKeys / 8 || k0 >= kr.end || !(k0 + 8 > kr.lo || k0 < S)) return 0;
         return __ldg(c.table + (size_t)u.row * c.width + (k0 >> c.ps_log2));
     };
     int pages = pages_of(0), pages_next = pages_of(1);
+    // Which groups are seen but have no page, for the softmax: written ahead of this thread's arrival for the tile's keys,
+    // which their products wait for.  The word of the tile four before has been read by then: an item written now (or
+    // sent three items ahead, E4M3) has waited for the keys of the tile three before it at least, whose products
+    // are only issued when the softmax has handed over the tile before them.
+    auto tell_gone = [&](uint32_t ring) {
+        const unsigned gone = __ballot_sync(~0u, (unsigned)pages >= (unsigned)c.pages);
+        if (tid == 0 && !(ring & 1)) sm.gone[(ring >> 1) % kGone] = gone;
+        return gone;
+    };
     // queries; without a map 16 (or 8) lanes for a row, zeros past the unit's rows (the copies of 64 KiB by
     // threads took 11000 clocks, longer than the sums they are to overlap)
     auto load_queries = [&]() {
@@ -444,10 +457,9 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
             const uint32_t ring = item + it;
             const int i = it >> 1, slot = ring % kSlots, k0 = kr.tile(u.ta + i) * kKeys;
             const uint8_t *base = it & 1 ? c.v : c.k;
-            // every key is seen by some token and has a page (the four warps hold the same page ids)
-            const bool whole = k0 + kKeys <= kr.end && (k0 >= kr.lo || k0 + kKeys <= S) &&
-                               __all_sync(~0u, lane >= kKeys / 8 || (unsigned)pages < (unsigned)c.pages);
             if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
+            // every key is seen by some token and has a page (the four warps hold the same page ids)
+            const bool whole = tell_gone(ring) == 0 && k0 + kKeys <= kr.end && (k0 >= kr.lo || k0 + kKeys <= S);
             if (whole) {
                 if (w == 0) {
                     if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kKeys * RB);
@@ -492,6 +504,7 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
         int sent = 0;   // items whose copies are under way
         auto send = [&]() {
             if (sent < 2 * n) {
+                tell_gone(item + sent);
                 const uint8_t *base = sent & 1 ? c.v : c.k;
                 uint8_t *dst = sm.raw[sent % kRaw] + tid * 16;
 #pragma unroll
@@ -613,10 +626,10 @@ __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const 
 }
 
 // ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far; `all_units`:
-// those of either half)
+// those of either half, `all_tiles`: their key tiles)
 template <int D, typename Q, bool FP8>
 __device__ bool softmax_unit(Smem<D, FP8> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
-                             uint32_t &tiles, uint32_t &units, uint32_t all_units)
+                             uint32_t &tiles, uint32_t &units, uint32_t all_units, uint32_t all_tiles)
 {
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, h = tid >> 7, rl = tid & 127, w = tid >> 5;
@@ -650,13 +663,20 @@ __device__ bool softmax_unit(Smem<D, FP8> &sm, const AttnParams &p, const Unit &
         uint32_t v[kKeys];
 #pragma unroll
         for (int q = 0; q < 4; q++) tmem_ld32_async(ts + 32 * q, v + 32 * q);
+        uint32_t gone;   // on its way beside them
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(gone) : "r"(smem_u32(&sm.gone[(all_tiles + i) % kGone])) : "memory");
 #pragma unroll
         for (int q = 0; q < 4; q++) tmem_wait_ld(v + 32 * q);
-        if (!all) {
+        if (!all || gone) {
             const int hi_j = pos - k0, lo_j = max(lo, k0) - k0, s_j = S - k0;
 #pragma unroll
             for (int j = 0; j < kKeys; j++)
                 if (!(j <= hi_j && (j >= lo_j || j < s_j))) v[j] = 0xff800000u;   // -inf
+            if (gone) {
+#pragma unroll
+                for (int j = 0; j < kKeys; j++)
+                    if (gone >> (j >> 3) & 1) v[j] = 0xff800000u;
+            }
         }
         float mx8[8];
 #pragma unroll
@@ -747,7 +767,7 @@ __device__ void softmax_role(Smem<D, FP8> &sm, const AttnParams &p, uint32_t tme
     int *count = reinterpret_cast<int *>(p.ws);
     SplitWs ws;
     ws.data = reinterpret_cast<float *>(p.ws + kAttnCounters * sizeof(int));
-    uint32_t tiles = 0, units = 0, all_units = 0, joins = 0;
+    uint32_t tiles = 0, units = 0, all_units = 0, all_tiles = 0, joins = 0;
     for (int k = 0; const Unit *at = unit_of(sm, k, p.c.err); k++) {
         const Unit &u = *at;
         float *partial = u.pieces > 1 ? ws.slot(u.slot, D) : nullptr;
@@ -759,8 +779,9 @@ __device__ void softmax_role(Smem<D, FP8> &sm, const AttnParams &p, uint32_t tme
                 if (p.lse) p.lse[row] = -INFINITY;
             }
         } else {
-            if (h < u.halves && !softmax_unit<D, Q, FP8>(sm, p, u, tmem, W, S, partial, tiles, units, all_units)) return;
+            if (h < u.halves && !softmax_unit<D, Q, FP8>(sm, p, u, tmem, W, S, partial, tiles, units, all_units, all_tiles)) return;
             all_units++;
+            all_tiles += u.tb - u.ta;
             if (partial) {
                 // the last of a unit's CTAs joins the pieces, in their order
                 __threadfence();
