@@ -383,8 +383,9 @@ kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t
  * sees are not read (their table entries may be -1, their contents anything); the value of
  * a key that is hidden from one token and seen by another of its sequence and call counts 0 times
  * for the first, so a NaN or an infinity in it can reach both.  Products are
- * taken in the query's type (a 16-bit cache must have it too; E4M3 codes are exact in both) with
- * FP32 sums; the softmax statistics are FP32.
+ * taken in 16 bits (the query's type, which a 16-bit cache must have too; halves with E4M3 codes,
+ * which are exact in them) with FP32 sums.  The weights exp(s_j - m) are rounded to that type before
+ * they multiply the values; m, the sum of the (unrounded) weights and lse are FP32.
  * Workspace: kda_attn_workspace_size() bytes, 256-byte aligned, ZEROED by the caller once; every
  * call leaves it ready for the next.  Calls that may overlap on the GPU need one each. */
 typedef struct {

@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                 }
                 // s[nb]: keys k0 + g (+ 8), rows nb * 8 + 2 cc (+ 1); in units of log2
                 const bool all = k0 + kStep - 1 <= p0 && (k0 >= lo_all || k0 + kStep <= S);
-                // The maximum is moved (by all of a row's lanes) only when a score passes it by more than 2^8: the
-                // usual step has no exchange between lanes.  P stays below 2^8, l and O have its scale.
+                // The maximum is moved (by all of a row's lanes) only when a score passes it by more than kGrow: the
+                // usual step has no exchange between lanes.  row_m is kShift below it; P, l and O have its scale.
                 bool grown = false;
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++) {
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                         if (!all && !key_visible(k0 + g + 8 * (i >> 1), row_pos[nb][i & 1], W, S)) s[nb][i] = -INFINITY;
                     }
 #pragma unroll
-                    for (int i = 0; i < 2; i++) grown |= fmaxf(s[nb][i], s[nb][i + 2]) * sc[nb][i] > row_m[nb][i] + 8.f;
+                    for (int i = 0; i < 2; i++) grown |= fmaxf(s[nb][i], s[nb][i + 2]) * sc[nb][i] > row_m[nb][i] + (P::kShift + P::kGrow);
                 }
                 if (__any_sync(~0u, grown)) {
 #pragma unroll
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                             float mx = fmaxf(s[nb][i], s[nb][i + 2]);
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-                            const float m_new = fmaxf(row_m[nb][i], mx * sc[nb][i]);
+                            const float m_new = fmaxf(row_m[nb][i], mx * sc[nb][i] - P::kShift);
                             const float alpha = m_new == -INFINITY ? 1.f : ex2(row_m[nb][i] - m_new);
                             row_m[nb][i] = m_new;
                             row_l[nb][i] *= alpha;
@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                         s[nb][i + 2] = ex2(fmaf(s[nb][i + 2], sc[nb][i], -base));
                         row_l[nb][i] += s[nb][i] + s[nb][i + 2];
                     }
-                    // P is rounded to the product's 16-bit type (relative error 2^-9 or 2^-12, as the
-                    // output's own rounding); l sums it unrounded
+                    // P is rounded to the product's 16-bit type (relative error 2^-8 or 2^-11, as the
+                    // output's own rounding; halves: down to 2^-25 of the largest); l sums it unrounded
                     pf[nb][0] = transpose8x8(P::pack(s[nb][0], s[nb][1]));
                     pf[nb][1] = transpose8x8(P::pack(s[nb][2], s[nb][3]));
                 }

@@ -5,9 +5,8 @@
 // order; a CTA takes 256 of them as two halves of 128 and walks the key tiles (128 keys) that its
 // tokens see.  Per half and tile: S = Q K^T into tensor memory, one thread per row takes the row's
 // maximum, P = exp2(S - m) back into tensor memory in 16 bits, O += P V with P as the tensor-memory
-// operand.  The running maximum m is only moved (and O rescaled) when it grows by more than 2^8: P
-// then stays below 2^8, which both 16-bit types hold with their full relative precision, and l and
-// O are FP32 sums of the same scale.
+// operand.  The running maximum m is only moved (and O rescaled) when it grows by more than 2^8 (2^4 where P
+// is half, see kShift): P stays in the range of its type, and l and O are FP32 sums of the same scale.
 //
 // Bound.  4 D flops for each visible (row, key) pair against D bytes moved once per 256 rows: the
 // tensor cores, or the 128 x 128 exponentials of each tile next to them.  Two halves, so that one
@@ -54,7 +53,6 @@ constexpr int kMaxSplits = 32;                 // pieces of a unit (their join r
 constexpr uint64_t kLimitNs = 2000000000ull;   // bound of every wait
 constexpr int kUnits = 2, kTable = 512;         // units on their way to the roles; sequences whose tile counts are kept on chip
 constexpr int kGone = 8;                       // tiles whose missing pages are told to the softmax (four would do, see load_unit)
-constexpr float kGrow = 8.f;                   // log2 growth of the maximum that O is rescaled for
 
 // What a CTA works on: rows [r0, r0 + rows) of the n * G of a sequence, and key tiles [ta, tb) of their range.
 struct Unit {
@@ -686,9 +684,9 @@ __device__ bool softmax_unit(Smem<D, FP8> &sm, const AttnParams &p, const Unit &
 #pragma unroll
             for (int x = 0; x < 8; x++) mx8[x] = fmaxf(fmaxf(mx8[x], __uint_as_float(v[j + x])), __uint_as_float(v[j + 8 + x]));
         const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])), fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float m_new = fmaxf(m, mx * sc);
+        const float m_new = fmaxf(m, P::kShift != 0.f ? fmaf(mx, sc, -P::kShift) : mx * sc);   // (m: kShift below the maximum)
         if (i == 0) m = m_new;
-        else if (__any_sync(~0u, m_new > m + kGrow)) {
+        else if (__any_sync(~0u, m_new > m + P::kGrow)) {
             // the products that wrote O are done: this tile's S was issued after them
             const float a = m_new == -INFINITY ? 1.f : ex2(m - m_new);
             l *= a;
