@@ -328,11 +328,18 @@ def _attn(cache: KdaKvCache, q, packed: bool, scale, window, sinks, out, lse, re
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     shape = q.shape
+    # plain numbers, so that a plan is found by their values (a tensor would be found by its identity)
+    if scale is not None and type(scale) is not float:
+        scale = float(scale)
+    if type(window) is not int:
+        window = int(window)
+    if type(sinks) is not int:
+        sinks = int(sinks)
 
     def make():
         ql = _tokens(q, "q", packed, None, cache)
         D = cache.head_dim
-        desc = _Desc(shape[-2], 1.0 / math.sqrt(D) if scale is None else float(scale), _i32(window, "window"), _i32(sinks, "sinks"), ql)
+        desc = _Desc(shape[-2], 1.0 / math.sqrt(D) if scale is None else scale, _i32(window, "window"), _i32(sinks, "sinks"), ql)
         return ctypes.byref(desc), shape[:-1]
 
     desc, rows_shape = _plan(cache, ("attn", packed, scale, window, sinks, q.dtype, q.device, shape, q.stride()), make)
