@@ -61,6 +61,9 @@ __device__ __forceinline__ void e4m3x4_half4(uint32_t w, uint32_t &lo, uint32_t 
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
+// What scores are multiplied with: 0 as the least that keeps hidden scores at -inf.  A NaN (of a scale in the cache) stays one.
+__device__ __forceinline__ float score_scale(float x) { return x < 1e-37f ? 1e-37f : x; }
+
 // With an E4M3 cache the products are taken in halves.  A bfloat16 row of queries is brought to a maximum in
 // [1, 2) by a power of two first (exact but for elements under 2^-14 of it, whose error stays under 2^-25 of
 // it): `mag` is the row's largest magnitude's bits; returns the factor `down` for the elements and `up` for

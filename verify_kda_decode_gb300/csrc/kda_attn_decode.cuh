@@ -280,8 +280,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         uint32_t qf[C::Q_SMEM ? 1 : D / 16][2];
         float sc[NB][2];      // scale of rows 2 cc, 2 cc + 1, in log2 units
         int row_pos[NB][2];   // and their tokens' positions
-        // (a scale of 0 as the least that keeps hidden scores at -inf)
-        const float sc_head = fmaxf(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f), 1e-37f);
+        const float sc_head = p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = nb * 8 + g;
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             }
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                sc[nb][i] = fmaxf(sc_head * (FP8 && !Q::is_half ? __shfl_sync(~0u, up, 4 * (2 * cc + i)) : 1.f), 1e-37f);
+                sc[nb][i] = score_scale(sc_head * (FP8 && !Q::is_half ? __shfl_sync(~0u, up, 4 * (2 * cc + i)) : 1.f));
                 row_pos[nb][i] = p0 + (mb * ROWS + nb * 8 + 2 * cc + i) / p.G;
             }
 #pragma unroll

@@ -642,8 +642,7 @@ __device__ bool softmax_unit(Smem<D, FP8> &sm, const AttnParams &p, const Unit &
         if (!wait_warp(sm, &sm.q_full[all_units & 1], (all_units >> 1) & 1, c.err)) return false;
         row_scale = sm.q_scale[all_units & 1][x];
     }
-    // (a scale of 0 as the least that keeps hidden scores at -inf)
-    const float sc = fmaxf(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f) * row_scale, 1e-37f);
+    const float sc = score_scale(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f) * row_scale);
     const int first = u.len - u.n;
     const int pos = first + row_token(p, u, min(x, u.rows - 1));  // this row's position
     const int lo = (int)max(-0x7fffffffll, (long long)pos - W + 1);
