@@ -409,7 +409,9 @@ kda_status kda_attn_decode(const kda_kv_cache *cache, int32_t layer, const kda_a
 /* Packed prefill: sequence b's new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of q, out
  * [total_tokens, num_q_heads, head_dim] and lse [total_tokens, num_q_heads] (or NULL); max_len
  * bounds every sequence's count (host; no device read).  A sequence whose offsets are out of
- * order or range, or longer than max_len, sets KDA_DEVERR_SEQLEN and is skipped. */
+ * order or range, or longer than max_len, sets KDA_DEVERR_SEQLEN and is skipped.  Offsets that
+ * decrease further away can make sequences share rows: the outputs are then undefined or not
+ * written, but no access leaves the arguments' extents. */
 kda_status kda_attn_prefill(const kda_kv_cache *cache, int32_t layer, const kda_attn_desc *desc,
                             const int32_t *rows, int32_t B, const int32_t *cu_seqlens,
                             int32_t total_tokens, int32_t max_len, const void *q, void *out,

@@ -823,15 +823,21 @@ __device__ void unit_role(SM &sm, const AttnParams &p, int W, int S)
     const int lane = threadIdx.x & 31;
     int *counter = reinterpret_cast<int *>(p.ws) + kMaxSplitCtas;   // next unit, CTAs that are done
     const int kept = min(p.B, kTable);
-    int all = sm.before[kept];
+    long long all = sm.before[kept];   // (2^36 at most)
     for (int b0 = kept; b0 < p.B; b0 += 32) {   // sequences past the table
         int c0, t = 0;
         if (b0 + lane < p.B) t = (prefill_seq(p, b0 + lane, c0, blockIdx.x == 0).n * p.G + kRowsCta - 1) / kRowsCta;
         all += __reduce_add_sync(~0u, t);
     }
+    // More row tiles than `total` tokens have: offsets that decrease let sequences share tokens.  Nothing is done then, so
+    // that tiles and units are counted in 32 bits below.
+    if (all > (long long)p.total * p.G / kRowsCta + p.B) {
+        if (blockIdx.x == 0 && lane == 0) atomicOr(c.err, KDA_DEVERR_SEQLEN);
+        all = 0;
+    }
     // Fewer units than CTAs: they are split over the keys.  (Splitting those of a partly filled last round as well
     // costs more than it saves: 16384 tokens in a 2048 window, 512 units for 152 CTAs, 125 us against 122.)
-    const long long n_units = (long long)all * c.Hkv;
+    const long long n_units = all * c.Hkv;
     const int splits = n_units > 0 && n_units * 2 <= gridDim.x ? min(kMaxSplits, (int)(gridDim.x / n_units)) : 1;
     const long long total = n_units * splits;
     long long idx = blockIdx.x;
@@ -846,7 +852,7 @@ __device__ void unit_role(SM &sm, const AttnParams &p, int W, int S)
             u.slot = (int)idx;         // (used where splits > 1: fewer than the CTAs then)
             u.first = u.slot - y;
             u.group = (int)unit;
-            const int want = all - 1 - x;   // the last row tiles first: the longest of a causal prompt
+            const int want = (int)all - 1 - x;   // the last row tiles first: the longest of a causal prompt
             int b = -1, tile = 0;
             if (want < sm.before[kept]) {
                 int a = 0, e = kept;        // the last sequence with before[] <= want, 32 at a time
