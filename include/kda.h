@@ -387,7 +387,8 @@ kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t
  * which are exact in them) with FP32 sums.  The weights exp(s_j - m) are rounded to that type before
  * they multiply the values; m, the sum of the (unrounded) weights and lse are FP32.
  * Workspace: kda_attn_workspace_size() bytes, 256-byte aligned, ZEROED by the caller once; every
- * call leaves it ready for the next.  Calls that may overlap on the GPU need one each. */
+ * call leaves it ready for the next, but for one that ends with KDA_DEVERR_TIMEOUT: it has to be
+ * zeroed again then.  Calls that may overlap on the GPU need one each. */
 typedef struct {
     int32_t num_q_heads;     /* a multiple of num_kv_heads, at most 64 per kv head */
     float scale;             /* finite, >= 0; usually 1 / sqrt(head_dim) */

@@ -30,3 +30,27 @@ def test_numbers_in_tensors_are_read_at_every_call(K):
         desc = K.paged._attn(c, q, False, scale, window, sinks, None, None, False)[0]._obj
         assert (desc.scale, desc.window, desc.sinks) == (s, w, n)
     assert len(c.__dict__["_plans"]) == 4   # by value: the last one is the first again
+
+
+@pytest.mark.parametrize("bits,cleared", [(0x4, True), (0x44, True), (0x40, False), (0, False)])
+def test_a_wait_that_gave_up_clears_the_own_workspace(K, monkeypatch, bits, cleared):
+    """Counters may be left above 0 by a call that ended so; reading its error makes the cache ready again."""
+    import contextlib
+
+    class Fake:
+        @staticmethod
+        def kda_kv_get_error(cache, host, stream):
+            host._obj.value = bits
+            return K.kda.KDA_ERR_DEVICE if bits else 0
+
+        kda_kv_workspace_size = K.library().kda_kv_workspace_size
+        kda_attn_workspace_size = K.library().kda_attn_workspace_size
+
+    c = cpu_cache(K)
+    c.c_struct()
+    c.__dict__["_attn_ws"][:64] = 1
+    monkeypatch.setattr(K.paged, "_lib", Fake)
+    monkeypatch.setattr(K.paged, "_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    assert K.kda_kv_get_error(c) == bits
+    assert bool(c.__dict__["_attn_ws"].any()) != cleared

@@ -15,7 +15,7 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from .kda import (KDA_ERR_DEVICE, KDA_OK, KDA_T_BF16, KDA_T_E4M3, KDA_T_F16, _call, _lib, _need, _ptr, _raise, _stream)
+from .kda import (KDA_DEVERR_TIMEOUT, KDA_ERR_DEVICE, KDA_OK, KDA_T_BF16, KDA_T_E4M3, KDA_T_F16, _call, _lib, _need, _ptr, _raise, _stream)
 
 _TYPES = {torch.bfloat16: KDA_T_BF16, torch.float16: KDA_T_F16, torch.float8_e4m3fn: KDA_T_E4M3}
 
@@ -357,7 +357,8 @@ def _attn(cache: KdaKvCache, q, packed: bool, scale, window, sinks, out, lse, re
 def kda_attn_decode(cache: KdaKvCache, layer: int, rows, q, scale: Optional[float] = None, window: int = 0,
                     sinks: int = 0, n_tokens=None, out=None, lse=None, return_lse: bool = False, workspace=None,
                     stream=None):
-    """Attention of the last T (1..16) tokens of each row over the layer's pages; q [B, T, Hq, D].
+    """Attention of the last T (1..16) tokens of each row over the layer's pages; q [B, T, Hq, D] (any strides, the
+    last dimension contiguous).  A workspace that is passed has to be zeroed once by its owner.
     Causal, or with a sliding window and sinks first tokens that stay visible.  n_tokens int32 [B]: only
     the first n of the T tokens count (entries past them are left as they were).  Returns out, or
     (out, lse f32 [B, T, Hq]) where lse is given or return_lse is set."""
@@ -377,7 +378,8 @@ def kda_attn_prefill(cache: KdaKvCache, layer: int, rows, cu_seqlens, max_len: i
                      window: int = 0, sinks: int = 0, out=None, lse=None, return_lse: bool = False, workspace=None,
                      stream=None):
     """Attention of packed new tokens: sequence b is rows cu_seqlens[b]..cu_seqlens[b+1]-1 of q [N, Hq, D],
-    the last tokens of cache row rows[b]; max_len bounds every count (host int, no device read).
+    the last tokens of cache row rows[b]; max_len bounds every count (host int, no device read).  q may have any
+    strides with a contiguous last dimension; a workspace that is passed has to be zeroed once by its owner.
     Returns out, or (out, lse f32 [N, Hq]) where lse is given or return_lse is set."""
     _, st, _, dev = cache._struct()
     pr, B = _rows(rows, dev)
@@ -390,11 +392,17 @@ def kda_attn_prefill(cache: KdaKvCache, layer: int, rows, cu_seqlens, max_len: i
 
 
 def kda_kv_get_error(cache: KdaKvCache, stream=None) -> int:
-    """Reads and clears the cache's device error word (synchronises the stream)."""
+    """Reads and clears the cache's device error word (synchronises the stream).  After KDA_DEVERR_TIMEOUT the
+    cache's own attention workspace is cleared as well; one that was passed has to be cleared by its owner."""
     _, st, _, dev = cache._struct()
     v = ctypes.c_int32(0)
     with torch.cuda.device(dev):
         r = _lib.kda_kv_get_error(st, ctypes.byref(v), _stream(stream, dev))
     if r not in (KDA_OK, KDA_ERR_DEVICE):
         _raise(r)
+    own = cache.__dict__.get("_attn_ws")
+    if v.value & KDA_DEVERR_TIMEOUT and own is not None:
+        own.zero_()
+        if own.is_cuda:
+            torch.cuda.current_stream(dev).synchronize()
     return int(v.value)
