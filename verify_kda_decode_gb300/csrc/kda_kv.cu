@@ -440,32 +440,37 @@ __device__ __forceinline__ void append_piece(const uint4 w, uint8_t *dst, float2
         *reinterpret_cast<uint4 *>(dst) = w;
     } else {
         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-        float f[8], q[8];
+        float g[8], q[8];   // g: the elements' negatives, for zeros' signs (below)
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             float2 v;
-            if constexpr (F16) v = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
-            else v = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u));
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
+            if constexpr (F16) {
+                const uint32_t y = x[i] ^ 0x80008000u;
+                v = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+            } else {
+                v = make_float2(__uint_as_float(x[i] << 16 ^ 0x80000000u), __uint_as_float((x[i] & 0xffff0000u) ^ 0x80000000u));
+            }
+            g[2 * i] = v.x;
+            g[2 * i + 1] = v.y;
         }
         // The code is the rounding of the IEEE quotient.  Markstein's theorem gives that quotient from the correctly
         // rounded reciprocal: q = f r, then q + (f - q scale) r, three packed operations for two elements
-        // (a division each took 57 us for 33000 tokens, bound by its instructions).  Infinities, and scales whose
+        // (a division each took 57 us for 33000 tokens, bound by its instructions); with f = -g as q - (q scale + g) r,
+        // whose inner sum is +0 where q is exact, so that a zero keeps its sign.  Infinities, and scales whose
         // reciprocal or products could leave the normal range (their reciprocal is given as NaN), take the
         // division.
         float t0 = 0.f, t1 = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             float e0, e1;
-            tc::mul2(q[i], q[i + 1], f[i], f[i + 1], scale.y, scale.y);
-            tc::fma2(e0, e1, q[i], q[i + 1], -scale.x, -scale.x, f[i], f[i + 1]);
-            tc::fma2(q[i], q[i + 1], e0, e1, scale.y, scale.y, q[i], q[i + 1]);
+            tc::mul2(q[i], q[i + 1], g[i], g[i + 1], -scale.y, -scale.y);
+            tc::fma2(e0, e1, q[i], q[i + 1], scale.x, scale.x, g[i], g[i + 1]);
+            tc::fma2(q[i], q[i + 1], e0, e1, -scale.y, -scale.y, q[i], q[i + 1]);
             tc::add2(t0, t1, t0, t1, q[i], q[i + 1]);
         }
         if (!(fabsf(t0 + t1) < 1e30f)) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) q[i] = __fdiv_rn(f[i], scale.x);
+            for (int i = 0; i < 8; i++) q[i] = __fdiv_rn(-g[i], scale.x);
         }
         uint32_t o[2];
 #pragma unroll
