@@ -317,7 +317,8 @@ typedef struct {
 } kda_kv_cache;
 
 /* Device scratch of the page calls below, owned by the caller, 256-byte aligned, no
- * initialisation needed.  Calls that may overlap on the GPU need scratch of their own. */
+ * initialisation needed.  Calls that may overlap on the GPU need scratch of their own.
+ * (kda_kv_truncate and kda_kv_fork check theirs as the others do; their kernels do not use it.) */
 size_t kda_kv_workspace_size(const kda_kv_cache *cache);
 
 /* Makes room for n_tokens[i] more tokens in row rows[i] (n_all where n_tokens is NULL) and adds

@@ -11,9 +11,9 @@
 //
 // Bound.  Every key and value byte is used for R rows only: HBM bound (R <= 32 needs at most 1/8 of
 // the tensor rate).  So the design is about bytes in flight and an even split.  Each warp owns a ring
-// of cp.async stages (16 keys and values a stage; 24 KiB a warp, 192 KiB an SM with eight warps,
-// against about 45 KiB that the latency-bandwidth product asks of an SM), with no CTA barrier inside
-// a run of keys.  All tiles of all (sequence, key head, row block) units are laid out in one line and
+// of cp.async stages (16 keys and values a stage; two to four stages, 12 to 24 KiB a warp, 8 to 16 warps and
+// 144 to 192 KiB an SM, see Cfg, against about 45 KiB that the latency-bandwidth product asks of an SM), with no
+// CTA barrier inside a run of keys.  All tiles of all (sequence, key head, row block) units are laid out in one line and
 // cut into equal runs, one per CTA, so ragged lengths load the SMs evenly; a unit that spans several
 // CTAs leaves partial (m, l, O) in the workspace and the CTA that finishes last joins them in the
 // fixed order of the pieces.  No result depends on which CTA that is.
@@ -37,11 +37,12 @@ constexpr int kUnitRows = 32;
 // sequences, four drafts, 1024 window: 70 us, with 2 / 4 / 8: 47 / 41 / 41 us; 131072 tokens of one
 // sequence: 91 us, 90 / 89 / 94 us.
 constexpr int kUnitCost = 4;
-// How many places longer a run may get for whole units to each CTA (see where the runs are made).  64 ragged
-// sequences in a 1024 window, 20 rows a unit: 35.3 us with cut units, 31.1 with whole ones (9 places more); 32 of 1024
-// tokens 21.0 and 17.5 us (12 more); 64 of 1024 tokens, 128 dims, two units a CTA: 50.4 and 53.1 us (18 more); 40
-// of 4096: 61 and 67 us (32 more).  One sequence, 8 key heads: of 300 tokens 9.3 and 7.5 us (8 more), of 517 tokens
-// 8.3 and 9.9 us (12 more).
+// How many places longer a run may get for whole units to each CTA (see where the runs are made); two numbers for all forms.
+// Measured both ways on 44 forms (16-bit and E4M3 caches, 64 and 128 dims, 1 to 100 sequences of 300 to 2048 tokens, 32
+// query and 8 key heads, one and four tokens): the 22 that get whole units gain 1 to 38 % by them, but for two that lose
+// 1.5 %; of the 22 that are cut, whole units would cost 17 forms 1 to 23 % (one sequence of 517 tokens, 12 places more: 8.5
+// us cut, 10.2 whole; of 300 tokens, 8 more: 9.2 and 7.7) and would gain five of 64 dims 2 to 16 %.  64 ragged sequences in a
+// 1024 window, 20 rows a unit: 35.3 us with cut units, 31.1 with whole ones (9 more).
 constexpr int kUneven = 12, kUnevenShort = 8;
 
 template <typename T>

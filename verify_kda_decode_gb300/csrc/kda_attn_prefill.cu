@@ -1063,7 +1063,8 @@ cudaError_t encode_pages(CUtensorMap *map, const void *base, const PagedCache &c
 
 // Queries as [token][head][D].  A map wants strides under 2^40 bytes, not 0, each a multiple of the one before it; queries
 // that have others (heads that share memory, heads farther apart than tokens), or that the encoder refuses for any
-// other reason, take the copies (4 x 4096 tokens: 445 us against 406 when the map came in).  (A dimension of one element may come with any stride, 0 too: it is not used.)
+// other reason, take the copies (4 x 4096 tokens: 445 us against 406 when the map came in).  A dimension of one
+// element may come with any stride, 0 too: it is not used.
 bool map_queries(CUtensorMap *map, const AttnParams &p)
 {
     if (kHalf % p.G) return false;

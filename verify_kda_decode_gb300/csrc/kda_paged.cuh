@@ -33,8 +33,8 @@ struct KvCall {
     int *remap;
 };
 
-// Scratch of the page calls, in ints: counters, eight arrays of `rows`, two lists of page ids.
-constexpr int kKvMeta = 16, kKvRowArrays = 8;
+// Scratch of the page calls, in ints: counters, seven arrays of `rows`, two lists of page ids.
+constexpr int kKvMeta = 16, kKvRowArrays = 7;
 inline size_t kv_workspace_ints(int rows, int pages) { return kKvMeta + (size_t)kKvRowArrays * rows + 2 * (size_t)pages; }
 
 cudaError_t launch_kv_extend(const KvCall &p, cudaStream_t stream);

@@ -4,7 +4,9 @@ Argument checks and marshalling only, in the manner of ``kda.py``: tensors are t
 calls run on the current stream of the cache's device with that device current.  A cache's own
 workspaces are made and cleared with it, before its constructor returns: its calls may run on any
 stream and be captured from the first one on.  Calls on one cache that may overlap on the GPU (two
-streams without an order between them) have to pass workspaces of their own.
+streams without an order between them) have to pass workspaces of their own.  Outputs that a call
+makes itself belong to the current stream: where ``stream`` names another one, order it after the
+current one first, or pass ``out`` (``lse``, ``remap``).
 """
 from __future__ import annotations
 
