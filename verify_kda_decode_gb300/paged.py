@@ -359,8 +359,8 @@ def _attn(cache: KdaKvCache, q, packed: bool, scale, window, sinks, out, lse, re
 def kda_attn_decode(cache: KdaKvCache, layer: int, rows, q, scale: Optional[float] = None, window: int = 0,
                     sinks: int = 0, n_tokens=None, out=None, lse=None, return_lse: bool = False, workspace=None,
                     stream=None):
-    """Attention of the last T (1..16) tokens of each row over the layer's pages; q [B, T, Hq, D] (any strides, the
-    last dimension contiguous).  A workspace that is passed has to be zeroed once by its owner.
+    """Attention of the last T (1..16) tokens of each row over the layer's pages; q [B, T, Hq, D] (strides in
+    multiples of 8 elements, the last dimension contiguous).  A workspace that is passed has to be zeroed once by its owner.
     Causal, or with a sliding window and sinks first tokens that stay visible.  n_tokens int32 [B]: only
     the first n of the T tokens count (entries past them are left as they were).  Returns out, or
     (out, lse f32 [B, T, Hq]) where lse is given or return_lse is set."""
@@ -381,7 +381,7 @@ def kda_attn_prefill(cache: KdaKvCache, layer: int, rows, cu_seqlens, max_len: i
                      stream=None):
     """Attention of packed new tokens: sequence b is rows cu_seqlens[b]..cu_seqlens[b+1]-1 of q [N, Hq, D],
     the last tokens of cache row rows[b]; max_len bounds every count (host int, no device read).  q may have any
-    strides with a contiguous last dimension; a workspace that is passed has to be zeroed once by its owner.
+    strides in multiples of 8 elements, its last dimension contiguous; a workspace that is passed has to be zeroed once by its owner.
     Returns out, or (out, lse f32 [N, Hq]) where lse is given or return_lse is set."""
     _, st, _, dev = cache._struct()
     pr, B = _rows(rows, dev)
