@@ -297,12 +297,16 @@ kda_status kda_get_error(const kda_pool *pool, int32_t *host_err, void *stream);
  * bits in *err_word and leave the sequence out.  All kernels are launched with programmatic
  * dependent launch and read nothing before their dependency wait. */
 
-/* Element types of queries, outputs and caches. */
-typedef enum { KDA_T_BF16 = 0, KDA_T_F16 = 1, KDA_T_E4M3 = 2 } kda_elem_type;
+/* Element types of queries, outputs and caches.  KDA_T_E2M1 is a cache's only: 4-bit codes with an E4M3 scale for each
+ * 16 elements of a head (see kda_kv_cache). */
+typedef enum { KDA_T_BF16 = 0, KDA_T_F16 = 1, KDA_T_E4M3 = 2, KDA_T_E2M1 = 4 } kda_elem_type;
 
 typedef struct {
     void *k, *v;             /* [num_layers, num_pages, num_kv_heads, page_size, head_dim], 16-byte
-                                aligned; kv_dtype */
+                                aligned; kv_dtype.  KDA_T_E2M1: a page's head is page_size * head_dim / 2
+                                bytes of codes, [page_size, head_dim / 2], element 2 i in the low four
+                                bits of byte i and 2 i + 1 in the high ones, then [page_size,
+                                head_dim / 16] E4M3 block scales */
     int32_t kv_dtype;        /* kda_elem_type */
     int32_t num_layers, num_pages, num_kv_heads;
     int32_t page_size;       /* 16, 32, 64 or 128 */
@@ -311,8 +315,9 @@ typedef struct {
     int32_t *page_table;     /* [rows, max_pages] */
     int32_t *seq_lens;       /* [rows] */
     int32_t *page_refs;      /* [num_pages] */
-    const float *k_scale;    /* [num_layers, num_kv_heads], needed with KDA_T_E4M3 (else ignored): */
-    const float *v_scale;    /*   a stored code c stands for scale * c; >= 0 */
+    const float *k_scale;    /* [num_layers, num_kv_heads], needed with KDA_T_E4M3 and KDA_T_E2M1 (else */
+    const float *v_scale;    /*   ignored): a stored code c stands for scale * c, or for scale * block
+                                  scale * c; >= 0 */
     int32_t *err_word;       /* device int32, zero-initialised by the caller */
 } kda_kv_cache;
 
@@ -355,12 +360,16 @@ kda_status kda_kv_compact(const kda_kv_cache *cache, int32_t *remap, void *works
                           size_t workspace_bytes, void *stream);
 
 /* Writes new keys and values of one layer into their pages (rounded to nearest even to E4M3 after
- * division by the layer's scale, clamped to +-448, where the cache holds codes; NaN stays NaN).
+ * division by the layer's scale, clamped to +-448, where the cache holds E4M3 codes; NaN stays NaN).
+ * In a KDA_T_E2M1 cache each 16 elements of a head share a scale: after division by the layer's scale
+ * the block scale is a sixth of their largest magnitude, rounded to E4M3 (2^-9 at least, 448 at most),
+ * and the codes are the quotients by it, rounded to nearest (ties to the even code) and clamped to +-6.
+ * A NaN makes its block's scale, and so the block, NaN.  All of it in FP32.
  * Either cu_seqlens is NULL and k, v hold B sequences of T tokens, of which the first
  * n_tokens[b] count (all T where n_tokens is NULL), seq_stride apart; or cu_seqlens [B+1] gives
  * sequence b the rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of T = total packed tokens.
  * A sequence with more new tokens than its row's length sets KDA_DEVERR_SEQLEN and is skipped.
- *   k, v      KDA_T_BF16 or KDA_T_F16 (the cache's own type, or either with an E4M3 cache), head
+ *   k, v      KDA_T_BF16 or KDA_T_F16 (the cache's own type, or either with a cache of codes), head
  *             h of token t at seq * seq_stride + t * token_stride + h * head_stride (elements;
  *             multiples of 8, pointers 16-byte aligned), head_dim elements contiguous */
 typedef struct {
@@ -374,6 +383,44 @@ kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t
                          const void *k, const kda_tokens_layout *k_layout, const void *v,
                          const kda_tokens_layout *v_layout, void *stream);
 
+/* Rotary positions.  Pair i (i < rotary_dim / 2) of a head's first rotary_dim elements is turned by
+ * the angle 2 pi * position * turns[i] / 2^64, and multiplied by `scale`:
+ *   a' = scale (a cos - b sin),  b' = scale (b cos + a sin);
+ * (a, b) are the elements i and i + rotary_dim / 2, or 2 i and 2 i + 1 where interleaved.  The other
+ * elements stay.  Scalings for long contexts are choices of the frequencies and of `scale`.  The
+ * product of position and frequency is taken modulo 2^64, so the angle keeps its precision (2^-24 of
+ * a turn) at any position; a negative position turns back.  The products are FP32, rounded once. */
+typedef struct {
+    const uint64_t *turns;   /* [rotary_dim / 2] (device): turns per position, in units of 2^-64 */
+    int32_t rotary_dim;      /* a multiple of 16, at most the head dim */
+    int32_t interleaved;     /* 0 or 1 */
+    float scale;             /* finite; 1 unless the scaling asks for another */
+} kda_rope_desc;
+
+/* Heads of a tensor and of its turned copy: one type, strides and alignment as for kda_kv_append.  The
+ * copy may be the tensor itself (the same pointer and strides); any other overlap is undefined.  Its tokens
+ * and heads must not share memory. */
+typedef struct {
+    int32_t num_heads;       /* 1 to 65536 */
+    kda_tokens_layout src, dst;
+} kda_rope_layout;
+
+/* Turns queries, and keys where k_layout is not NULL, of B sequences of T tokens: positions int32 [B, T].
+ * head_dim: a multiple of 16, at most 512.  B * T = 0 is a no-op. */
+kda_status kda_rope(const kda_rope_desc *rope, int32_t head_dim, const int32_t *positions, int32_t B,
+                    int32_t T, const kda_rope_layout *q_layout, const void *q, void *q_out,
+                    const kda_rope_layout *k_layout, const void *k, void *k_out, void *stream);
+
+/* kda_kv_append of keys that are turned on the way, by their positions in the row, and, where q_layout is not
+ * NULL, the new tokens' queries with them: q_out gets the turned queries in their type; keys go to the cache
+ * from FP32, rounded once.  With cu_seqlens q and q_out are packed as k and v are.  Sequences that are
+ * skipped, tokens that do not count and tokens without a page leave their part of q_out as it was. */
+kda_status kda_kv_append_rope(const kda_kv_cache *cache, int32_t layer, const kda_rope_desc *rope,
+                              const int32_t *rows, int32_t B, int32_t T, const int32_t *n_tokens,
+                              const int32_t *cu_seqlens, const kda_rope_layout *q_layout, const void *q,
+                              void *q_out, const void *k, const kda_tokens_layout *k_layout, const void *v,
+                              const kda_tokens_layout *v_layout, void *stream);
+
 /* Attention of new tokens over a layer's pages.  A token at position p sees key j where j <= p and
  * (window == 0, or j > p - window, or j < sinks): a causal layer, or one with a sliding window
  * of `window` keys (the token's own among them) and `sinks` first tokens that stay visible.
@@ -384,8 +431,8 @@ kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t
  * sees are not read (their table entries may be -1, their contents anything); the value of
  * a key that is hidden from one token and seen by another of its sequence and call counts 0 times
  * for the first, so a NaN or an infinity in it can reach both.  Products are
- * taken in 16 bits (the query's type, which a 16-bit cache must have too; halves with E4M3 codes,
- * which are exact in them) with FP32 sums.  The weights exp(s_j - m) are rounded to that type before
+ * taken in 16 bits (the query's type, which a 16-bit cache must have too; halves with E4M3 codes
+ * and with E2M1 codes times their block scale, both exact in them) with FP32 sums.  The weights exp(s_j - m) are rounded to that type before
  * they multiply the values; m, the sum of the (unrounded) weights and lse are FP32.
  * Workspace: kda_attn_workspace_size() bytes, 256-byte aligned, ZEROED by the caller once; every
  * call leaves it ready for the next, but for one that ends with KDA_DEVERR_TIMEOUT: it has to be

@@ -8,6 +8,9 @@ namespace kda {
 
 constexpr float kLn2 = 0.693147180559945309f;
 
+// What a cache holds: 16-bit elements, E4M3 codes, or E2M1 codes with an E4M3 scale for each 16 elements.
+constexpr int kKv16 = 0, kKvE4M3 = 1, kKvE2M1 = 2;
+
 // Keys that tokens at positions [p0, p1] (p1 >= p0) of a row of `len` tokens see, as tiles of kTile
 // keys: tiles [0, st) hold the sinks, then tiles from `first` to the last one needed.  A token at p
 // sees j <= p with p - j < W or j < S (W = INT_MAX without a window, S then 0).
@@ -59,6 +62,26 @@ __device__ __forceinline__ void e4m3x4_half4(uint32_t w, uint32_t &lo, uint32_t 
 {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// Two E4M3 codes (the low 16 bits) -> two halves, exact.
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t w)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+// Eight E2M1 codes, the first in the lowest bits -> eight halves in order, exact.
+__device__ __forceinline__ void e2m1x8_half8(uint32_t w, uint32_t *h)
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // What scores are multiplied with: 0 as the least that keeps hidden scores at -inf.  A NaN (of a scale in the cache) stays one.

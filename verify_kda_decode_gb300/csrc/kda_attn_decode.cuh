@@ -79,12 +79,31 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
     return v;
 }
 
-template <int D, bool FP8, int NB>
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <int D, int KV, int NB>
 struct Cfg {
-    static constexpr int ES = FP8 ? 1 : 2;
-    static constexpr int RB = D * ES;                     // bytes of a key
-    static constexpr int CH = RB / 16;                    // its 16-byte chunks
-    static constexpr int STAGE = 2 * kStep * RB;          // keys, then values
+    static constexpr int RB = KV == kKv16 ? D * 2 : KV == kKvE4M3 ? D : D / 2;   // bytes of a key (its codes)
+    static constexpr int SB = KV == kKvE2M1 ? D / 16 : 0; // ... and of its block scales
+    static constexpr int CH = RB / 16;                    // 16-byte chunks of a key
+    static constexpr int STAGE = 2 * kStep * (RB + SB);   // keys, values, then both's block scales
     // CTAs of an SM: as many as the accumulators (D NB / 4 registers) leave room for.  A warp's step is a
     // chain of latencies (scores, exponentials, product), which other warps cover: two CTAs everywhere
     // against this, 64 x 4096 tokens, 8 heads, E4M3: 153 us, 129 us; bfloat16 (HBM bound) 171 us both.
@@ -100,9 +119,16 @@ struct Cfg {
     // chunk c of row r is stored at chunk c ^ swz(r): conflict-free for the fragment loads
     // (K: eight lanes read four chunks of two rows; V: two chunks of four even rows)
     static __device__ __forceinline__ int swz_k(int r) { return CH >= 8 ? 4 * (r & 1) : 0; }
-    static __device__ __forceinline__ int swz_v(int r) { return CH >= 8 ? 2 * ((r >> 1) & 3) : (r >> 1) & 3; }
+    static __device__ __forceinline__ int swz_v(int r) { return KV == kKvE2M1 ? 0 : CH >= 8 ? 2 * ((r >> 1) & 3) : (r >> 1) & 3; }
+    // where chunk c of value row r of an E2M1 step is stored: its rows are shorter than the banks are wide, so the
+    // chunks of the 128 bytes that hold 2 (or 4) rows change places (lanes read 8, or 4, bytes of every second row)
+    static __device__ __forceinline__ int v_at(int r, int c)
+    {
+        return D == 128 ? (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (2 * ((r >> 1) & 3))) * 16)
+                        : (r >> 2) * 128 + ((((r & 3) * 2 + c) ^ (2 * ((r >> 2) & 1))) * 16);
+    }
     // head dim of the first of the two elements that accumulator block m of lane group g holds
-    static __device__ __forceinline__ int dim(int m, int g) { return FP8 ? (D / 8) * g + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3); }
+    static __device__ __forceinline__ int dim(int m, int g) { return KV != kKv16 ? (D / 8) * g + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3); }
 };
 
 struct Partials {   // workspace: counters, then for each CTA two slots of (m, l, O)
@@ -130,6 +156,13 @@ __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const uint8_t *src, b
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
 
+// N (4 or 8) bytes
+template <int N>
+__device__ __forceinline__ void cp_scales(uint32_t dst, const uint8_t *src, bool read)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(read ? N : 0) : "memory");
+}
+
 // Runs of tiles are counted in 64 bits (rows that share pages can hold more keys than memory); the
 // divisions take the 32-bit path whenever the numbers allow it.
 __device__ __forceinline__ long long div_pos(long long a, long long b)
@@ -137,11 +170,14 @@ __device__ __forceinline__ long long div_pos(long long a, long long b)
     return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-template <int D, typename Q, bool FP8, int NB>
-__global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decode_kernel(const AttnParams p)
+template <int D, typename Q, int KV, int NB>
+__global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode_kernel(const AttnParams p)
 {
-    using C = Cfg<D, FP8, NB>;
-    using P = std::conditional_t<FP8, Half, Q>;   // type of both products: E4M3 codes are exact halves
+    using C = Cfg<D, KV, NB>;
+    constexpr bool CODES = KV != kKv16;
+    // type of both products: E4M3 codes are exact halves, and so are E2M1 codes times their E4M3 scale (two bits by
+    // four, 2^-10 to 2688)
+    using P = std::conditional_t<CODES, Half, Q>;
     constexpr int kSeqs = 256;                    // sequences whose (row, length, tokens) are kept on chip
     constexpr int MT = D / 16;                    // accumulator blocks (16 head dims)
     constexpr int ROWS = 8 * NB;
@@ -271,17 +307,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         const KeyRange<kTileKeys> kr(p0, seq.len - 1, seq.len, W, S);
         const int lo_all = (int)max(0ll, (long long)seq.len - W);         // every token sees [lo_all, p0]
         const uint32_t page_bytes = (uint32_t)c.page_bytes();   // under 2^27
-        const uint8_t *k_base = c.k + ((size_t)p.layer * c.pages * c.Hkv + h) * ((size_t)c.ps * C::RB) + lane * 16;
+        const uint8_t *k_head = c.k + ((size_t)p.layer * c.pages * c.Hkv + h) * ((size_t)c.ps * (C::RB + C::SB)), *k_base = k_head + lane * 16;
         const ptrdiff_t v_minus_k = c.v - c.k;
+        // E2M1: lanes 0 to 15 copy the block scales of a step's keys, the others those of its values
+        const uint8_t *sc_base = k_head + (lane < kStep ? 0 : v_minus_k) + (size_t)c.ps * C::RB + (lane % kStep) * C::SB;
+        const uint32_t dst_s = 2 * kStep * C::RB + lane * C::SB;
         // where a lane's pieces go: the swizzles of a step's rows differ from its first row's by constants
         const uint32_t dst_k = (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_k(lane / C::CH)) * 16);
-        const uint32_t dst_v = (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_v(lane / C::CH)) * 16);
+        const uint32_t dst_v = KV == kKvE2M1 ? C::v_at(lane / C::CH, lane % C::CH)
+                                             : (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_v(lane / C::CH)) * 16);
 
         // queries: rows nb * 8 + g, the elements this thread multiplies
         uint32_t qf[C::Q_SMEM ? 1 : D / 16][2];
         float sc[NB][2];      // scale of rows 2 cc, 2 cc + 1, in log2 units
         int row_pos[NB][2];   // and their tokens' positions
-        const float sc_head = p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
+        const float sc_head = p.scale_log2 * (CODES ? c.k_scale[p.layer * c.Hkv + h] : 1.f);
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = nb * 8 + g;
@@ -290,12 +330,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             uint4 x[D / 32];
 #pragma unroll
             for (int j = 0; j < D / 32; j++) {
-                // 16-bit cache: chunk cc + 4 j of 8 elements; E4M3: 16-element chunks, this is half (j & 1) of chunk cc + 4 (j / 2)
-                const int e = FP8 ? 16 * (cc + 4 * (j >> 1)) + 8 * (j & 1) : 8 * (cc + 4 * j);
+                // 16-bit cache: chunk cc + 4 j of 8 elements; E4M3: 16-element chunks, this is half (j & 1) of chunk cc + 4 (j / 2);
+                // E2M1: a quarter of the key
+                const int e = KV == kKv16 ? 8 * (cc + 4 * j) : KV == kKvE4M3 ? 16 * (cc + 4 * (j >> 1)) + 8 * (j & 1) : (D / 4) * cc + 8 * j;
                 x[j] = r < n_rows ? __ldg(reinterpret_cast<const uint4 *>(src + e)) : make_uint4(0, 0, 0, 0);
             }
             float up = 1.f;
-            if constexpr (FP8 && !Q::is_half) {
+            if constexpr (CODES && !Q::is_half) {
                 uint32_t mag = 0;
 #pragma unroll
                 for (int j = 0; j < D / 32; j++) mag = max_magnitude(mag, x[j]);
@@ -308,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
             }
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                sc[nb][i] = score_scale(sc_head * (FP8 && !Q::is_half ? __shfl_sync(~0u, up, 4 * (2 * cc + i)) : 1.f));
+                sc[nb][i] = score_scale(sc_head * (CODES && !Q::is_half ? __shfl_sync(~0u, up, 4 * (2 * cc + i)) : 1.f));
                 row_pos[nb][i] = p0 + (mb * ROWS + nb * 8 + 2 * cc + i) / p.G;
             }
 #pragma unroll
@@ -381,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                                 cp16(dk + i * 512, sk + i * 512);
                                 cp16(dv + i * 512 + (dst_v ^ (C::swz_v(i * PER) * 16)), sv + i * 512);
                             }
+                            if constexpr (KV == kKvE2M1) cp_scales<C::SB>(ring + stage * C::STAGE + dst_s, sc_base + (size_t)(uint32_t)page * page_bytes + (k0 & (c.ps - 1)) * C::SB, true);
                         } else {   // zeros for the keys that no token sees
 #pragma unroll
                             for (int i = 0; i < kStep / PER; i++) {
@@ -388,6 +430,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                                 const bool read = j < kr.end && (j >= kr.lo || j < S);
                                 cp16_or_zero(dk + i * 512, sk + i * 512, read);
                                 cp16_or_zero(dv + i * 512 + (dst_v ^ (C::swz_v(i * PER) * 16)), sv + i * 512, read);
+                            }
+                            if constexpr (KV == kKvE2M1) {
+                                const int j = k0 + lane % kStep;
+                                cp_scales<C::SB>(ring + stage * C::STAGE + dst_s, sc_base + (size_t)(uint32_t)page * page_bytes + (k0 & (c.ps - 1)) * C::SB,
+                                                 j < kr.end && (j >= kr.lo || j < S));
                             }
                         }
                     }
@@ -422,24 +469,54 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                         mma16816<P>(NB == 1 && (kb_ & 1) ? s2[nb] : s[nb], a, q.x, q.y);
                     }
                 };
-#pragma unroll
-                for (int j = 0; j < C::CH / 4; j++) {
-                    const uint4 x = lds128(kb + g * C::RB + (((cc + 4 * j) ^ C::swz_k(g)) * 16));
-                    const uint4 y = lds128(kb + (g + 8) * C::RB + (((cc + 4 * j) ^ C::swz_k(g + 8)) * 16));
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int u = 0; u < 4; u++) {
-                            uint32_t a[4];
-                            e4m3x4_half4(xs[u], a[0], a[2]);
-                            e4m3x4_half4(ys[u], a[1], a[3]);
-                            qk(4 * j + u, a);
-                        }
+                if constexpr (KV == kKvE2M1) {
+                    // a quarter of the key for each lane, one or two blocks of 16 elements
+                    constexpr int NW = D / 32;
+                    uint32_t xs[NW], ys[NW], sx[2], sy[2];
+                    const uint32_t ks = kb + 2 * kStep * C::RB;
+                    if constexpr (D == 128) {
+                        const uint4 x = lds128(kb + g * C::RB + cc * 16), y = lds128(kb + (g + 8) * C::RB + cc * 16);
+                        xs[0] = x.x, xs[1] = x.y, xs[2] = x.z, xs[3] = x.w;
+                        ys[0] = y.x, ys[1] = y.y, ys[2] = y.z, ys[3] = y.w;
+                        const uint32_t a = e4m3x2_half2(lds_u16(ks + g * C::SB + 2 * cc)), b = e4m3x2_half2(lds_u16(ks + (g + 8) * C::SB + 2 * cc));
+                        sx[0] = __byte_perm(a, a, 0x1010), sx[1] = __byte_perm(a, a, 0x3232);
+                        sy[0] = __byte_perm(b, b, 0x1010), sy[1] = __byte_perm(b, b, 0x3232);
                     } else {
+                        const uint2 x = lds64(kb + g * C::RB + cc * 8), y = lds64(kb + (g + 8) * C::RB + cc * 8);
+                        xs[0] = x.x, xs[1] = x.y, ys[0] = y.x, ys[1] = y.y;
+                        sx[0] = e4m3x2_half2(lds_u8(ks + g * C::SB + cc) * 0x101u), sy[0] = e4m3x2_half2(lds_u8(ks + (g + 8) * C::SB + cc) * 0x101u);
+                    }
 #pragma unroll
-                        for (int u = 0; u < 2; u++) {
-                            const uint32_t a[4] = {xs[2 * u], ys[2 * u], xs[2 * u + 1], ys[2 * u + 1]};
-                            qk(2 * j + u, a);
+                    for (int u = 0; u < NW; u++) {
+                        uint32_t x[4], y[4];
+                        e2m1x8_half8(xs[u], x);
+                        e2m1x8_half8(ys[u], y);
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const uint32_t a[4] = {hmul2(x[2 * i], sx[u / 2]), hmul2(y[2 * i], sy[u / 2]), hmul2(x[2 * i + 1], sx[u / 2]), hmul2(y[2 * i + 1], sy[u / 2])};
+                            qk(2 * u + i, a);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < C::CH / 4; j++) {
+                        const uint4 x = lds128(kb + g * C::RB + (((cc + 4 * j) ^ C::swz_k(g)) * 16));
+                        const uint4 y = lds128(kb + (g + 8) * C::RB + (((cc + 4 * j) ^ C::swz_k(g + 8)) * 16));
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                        if constexpr (CODES) {
+#pragma unroll
+                            for (int u = 0; u < 4; u++) {
+                                uint32_t a[4];
+                                e4m3x4_half4(xs[u], a[0], a[2]);
+                                e4m3x4_half4(ys[u], a[1], a[3]);
+                                qk(4 * j + u, a);
+                            }
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 2; u++) {
+                                const uint32_t a[4] = {xs[2 * u], ys[2 * u], xs[2 * u + 1], ys[2 * u + 1]};
+                                qk(2 * j + u, a);
+                            }
                         }
                     }
                 }
@@ -496,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
 #pragma unroll
                     for (int nb = 0; nb < NB; nb++) mma16816<P>(acc[m][nb], a, pf[nb][0], pf[nb][1]);
                 };
-                if constexpr (!FP8) {
+                if constexpr (!CODES) {
 #pragma unroll
                     for (int hh = 0; hh < D / 64; hh++) {
                         uint32_t v[4][4];
@@ -507,6 +584,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
                         }
 #pragma unroll
                         for (int i = 0; i < 4; i++) pv(4 * hh + i, v[0][i], v[1][i], v[2][i], v[3][i]);
+                    }
+                } else if constexpr (KV == kKvE2M1) {
+                    constexpr int NW = D / 64;   // words of 8 codes per thread and key, all of one block
+                    uint32_t v[4][NW], sv[4];
+                    const uint32_t vs = vb + kStep * (C::RB + C::SB);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if constexpr (NW == 2) {
+                            const uint2 x = lds64(vb + C::v_at(kk[i], g >> 1) + 8 * (g & 1));
+                            v[i][0] = x.x, v[i][1] = x.y;
+                            sv[i] = lds_u8(vs + kk[i] * C::SB + g);
+                        } else {
+                            v[i][0] = lds32(vb + C::v_at(kk[i], g >> 2) + 4 * (g & 3));
+                            sv[i] = lds_u8(vs + kk[i] * C::SB + (g >> 1));
+                        }
+                    }
+                    const uint32_t s01 = e4m3x2_half2(sv[0] | sv[1] << 8), s23 = e4m3x2_half2(sv[2] | sv[3] << 8);
+#pragma unroll
+                    for (int u = 0; u < NW; u++) {
+                        // the same element's codes of two keys in one byte before the conversion
+                        uint32_t e[2][2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const uint32_t x = v[2 * i][u], y = v[2 * i + 1][u];
+                            e2m1x8_half8((x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u), e[0][i]);
+                            e2m1x8_half8((x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), e[1][i]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const uint32_t a[4] = {hmul2(e[0][0][j], s01), hmul2(e[1][0][j], s01), hmul2(e[0][1][j], s23), hmul2(e[1][1][j], s23)};
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++) mma16816<P>(acc[4 * u + j][nb], a, pf[nb][0], pf[nb][1]);
+                        }
                     }
                 } else {
                     constexpr int NW = D / 32;   // words of 4 codes per thread and key
@@ -567,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
         __syncthreads();
 
         const int f = (int)div_pos(u0, chunk), l = (int)div_pos(u0 + kt - 1, chunk);   // CTAs that hold the unit's pieces
-        const float v_scale = FP8 ? c.v_scale[p.layer * c.Hkv + h] : 1.f;
+        const float v_scale = CODES ? c.v_scale[p.layer * c.Hkv + h] : 1.f;
         auto store = [&](int r, int d, float4 o, float l_sum, float m) {   // 4 outputs of a row
             const int t = (mb * ROWS + r) / p.G, hq = h * p.G + (mb * ROWS + r) % p.G;
             const size_t row = ((size_t)b * p.T + t) * p.Hq + hq;
@@ -664,38 +774,37 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, NB>::OCC) kda_attn_decod
     }
 }
 
-template <int D, typename Q, bool FP8, int NB>
+template <int D, typename Q, int KV, int NB>
 cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr int smem = Cfg<D, FP8, NB>::SMEM;
-    static_assert(Cfg<D, FP8, NB>::NS >= 2 && Cfg<D, FP8, NB>::NS <= 32, "a ring of two stages at least");
+    constexpr int smem = Cfg<D, KV, NB>::SMEM;
+    static_assert(Cfg<D, KV, NB>::NS >= 2 && Cfg<D, KV, NB>::NS <= 32, "a ring of two stages at least");
     int resident = 0;
-    const cudaError_t e = setup.get(kda_attn_decode_kernel<D, Q, FP8, NB>, kThreads, smem, 0, &resident);
+    const cudaError_t e = setup.get(kda_attn_decode_kernel<D, Q, KV, NB>, kThreads, smem, 0, &resident);
     if (e != cudaSuccess) return e;
     if (resident < 1) return cudaErrorLaunchOutOfResources;
-    return launch_pdl(kda_attn_decode_kernel<D, Q, FP8, NB>, dim3((unsigned)min(resident, kMaxCtas)), dim3(kThreads), smem, stream, p);
+    return launch_pdl(kda_attn_decode_kernel<D, Q, KV, NB>, dim3((unsigned)min(resident, kMaxCtas)), dim3(kThreads), smem, stream, p);
 }
 
 // Row blocks of 8, 16, 24 or 32: the smallest that holds the rows of a sequence and key head, at most 32
 // (more rows read the keys again from L2).  A step's instructions grow with the block: 20 rows, 64 sequences in
 // a 1024 window: 41 us with 32, 36 us with 24 (and without the second
 // chain of products and the separate scaling that both had).
-template <int D, typename Q, bool FP8>
+template <int D, typename Q, int KV>
 cudaError_t launch_rows(const AttnParams &p, cudaStream_t stream)
 {
     const int rows = p.T * p.G;
-    if (rows <= 8) return launch_as<D, Q, FP8, 1>(p, stream);
-    if (rows <= 16) return launch_as<D, Q, FP8, 2>(p, stream);
-    if (rows <= 24) return launch_as<D, Q, FP8, 3>(p, stream);
-    return launch_as<D, Q, FP8, 4>(p, stream);
+    if (rows <= 8) return launch_as<D, Q, KV, 1>(p, stream);
+    if (rows <= 16) return launch_as<D, Q, KV, 2>(p, stream);
+    if (rows <= 24) return launch_as<D, Q, KV, 3>(p, stream);
+    return launch_as<D, Q, KV, 4>(p, stream);
 }
 
-template <int D>
+template <int D, int KV>
 cudaError_t launch_types(const AttnParams &p, cudaStream_t stream)
 {
-    if (p.c.dtype == KDA_T_E4M3) return p.f16 ? launch_rows<D, Half, true>(p, stream) : launch_rows<D, Bf16, true>(p, stream);
-    return p.f16 ? launch_rows<D, Half, false>(p, stream) : launch_rows<D, Bf16, false>(p, stream);
+    return p.f16 ? launch_rows<D, Half, KV>(p, stream) : launch_rows<D, Bf16, KV>(p, stream);
 }
 
 }  // namespace

@@ -66,14 +66,21 @@ struct Unit {
     int slot, first, group;   // ... this piece's and the first one's place in the workspace, the split unit's number
 };
 
-// A ring of four tiles; with an E4M3 cache three, and three fetches of codes on their way to it.
-template <int D, bool FP8>
+// Bytes of a key: its elements or codes, and its block scales (E2M1).
+template <int D, int KV>
+struct KeyBytes {
+    static constexpr int RB = KV == kKv16 ? D * 2 : KV == kKvE4M3 ? D : D / 2, SB = KV == kKvE2M1 ? D / 16 : 0;
+};
+
+// A ring of four tiles; with a cache of codes three, and three fetches of codes on their way to it.
+template <int D, int KV>
 struct Smem {
-    static constexpr uint32_t kSlots = FP8 ? 3 : 4;
+    static constexpr uint32_t kSlots = KV != kKv16 ? 3 : 4;
     static constexpr int kRaw = 3;
     uint8_t q[2][kHalf * D * 2];
     uint8_t kv[kSlots][kKeys * D * 2];
-    uint8_t raw[FP8 ? kRaw : 1][FP8 ? kKeys * D : 16];
+    uint8_t raw[KV != kKv16 ? kRaw : 1][KV != kKv16 ? kKeys * KeyBytes<D, KV>::RB : 16];
+    uint8_t raw_scale[KV == kKvE2M1 ? kRaw : 1][KV == kKvE2M1 ? kKeys * KeyBytes<D, KV>::SB : 16];
     uint64_t q_full[2], q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
     unsigned gone[kGone];                   // by the tile's number: groups of 8 keys that are seen but have no page
     Unit unit[kUnits];
@@ -348,20 +355,21 @@ __device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, 
 
 // ---- warps 8-11: a unit's queries, then keys and values of tile i as ring items 2 i and 2 i + 1
 // (`item`: ring items so far, `units`: units so far)
-template <int D, typename Q, bool FP8>
-__device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int W, int S, uint32_t &item, uint32_t &units)
+template <int D, typename Q, int KV>
+__device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int W, int S, uint32_t &item, uint32_t &units)
 {
     const AttnParams &p = args.p;
-    constexpr uint32_t kSlots = Smem<D, FP8>::kSlots;
+    constexpr uint32_t kSlots = Smem<D, KV>::kSlots;
     const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
     const PagedCache &c = p.c;
     const int tid = threadIdx.x - kSoftmax, w = tid >> 5, lane = tid & 31, r8 = lane & 7, q4 = lane >> 3;
     const int n = u.tb - u.ta;
-    constexpr int ES = FP8 ? 1 : 2, RB = D * ES;
+    constexpr bool CODES = KV != kKv16;
+    constexpr int RB = KeyBytes<D, KV>::RB, SB = KeyBytes<D, KV>::SB;
     constexpr int CPR = RB / 16;              // 16-byte chunks of a key
     constexpr int PASS = CPR / 4;             // passes of four chunks over a group of 8 keys
     constexpr int GR = kKeys / 8 / 4;         // groups of 8 keys of a warp: w, w + 4, ...
-    const size_t head_bytes = (size_t)c.ps * RB;
+    const size_t head_bytes = (size_t)c.ps * (RB + SB);
     // page of key group `lane` (16 groups of a tile), 0 where none of its keys is seen (and no page is looked at)
     auto pages_of = [&](int i) {
         const int k0 = kr.tile(u.ta + i) * kKeys + lane * 8;
@@ -382,7 +390,7 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
     // threads took 11000 clocks, longer than the sums they are to overlap)
     auto load_queries = [&]() {
         if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
-        if constexpr (FP8 && !Q::is_half) {   // through registers, as halves
+        if constexpr (CODES && !Q::is_half) {   // through registers, as halves
             constexpr int LPR = D / 8, STEP = kLoaders / LPR;
             const int g = tid % LPR;
             const uint16_t *base = p.q + (long long)u.c0 * p.ql.token + (long long)(u.h * p.G) * p.ql.head + g * 8;
@@ -435,22 +443,22 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
         return true;
     };
     auto queries_done = [&]() {
-        if (args.q_map && !(FP8 && !Q::is_half)) return;
+        if (args.q_map && !(CODES && !Q::is_half)) return;
         cp_async_wait_all();
         tc::fence_smem_to_async();
         mbar_arrive(&sm.q_full[units & 1]);
     };
-    // source of this lane's key of group gi of tile i; null where nothing is read
-    auto source = [&](const uint8_t *base, int i, int gi, int pg) -> const uint8_t * {
-        const int k0 = kr.tile(u.ta + i) * kKeys + gi * 8, j = k0 + r8;
+    // source of key r of group gi of tile i, this many bytes a key from `at` on in its page; null where nothing is read
+    auto source = [&](const uint8_t *base, int i, int gi, int pg, int r, size_t at, int bytes) -> const uint8_t * {
+        const int k0 = kr.tile(u.ta + i) * kKeys + gi * 8, j = k0 + r;
         if (!(j < kr.end && (j >= kr.lo || j < S))) return nullptr;
         if ((unsigned)pg >= (unsigned)c.pages) {
             atomicOr(c.err, KDA_DEVERR_PAGE);
             return nullptr;
         }
-        return base + (((size_t)p.layer * c.pages + pg) * c.Hkv + u.h) * head_bytes + (size_t)(j & (c.ps - 1)) * RB;
+        return base + (((size_t)p.layer * c.pages + pg) * c.Hkv + u.h) * head_bytes + at + (size_t)(j & (c.ps - 1)) * bytes;
     };
-    if constexpr (!FP8) {
+    if constexpr (!CODES) {
         for (int it = 0; it < 2 * n; it++) {
             const uint32_t ring = item + it;
             const int i = it >> 1, slot = ring % kSlots, k0 = kr.tile(u.ta + i) * kKeys;
@@ -476,7 +484,7 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
 #pragma unroll
                 for (int a = 0; a < GR; a++) {
                     const int gi = w + 4 * a;
-                    const uint8_t *src = source(base, i, gi, __shfl_sync(~0u, pages, gi));
+                    const uint8_t *src = source(base, i, gi, __shfl_sync(~0u, pages, gi), r8, 0, RB);
 #pragma unroll
                     for (int x = 0; x < PASS; x++)
                         cp_async16(sm.kv[slot] + chunk_at(gi * 8 + r8, x * 4 + q4), src ? src + (x * 4 + q4) * 16 : c.k, src ? 16 : 0);
@@ -498,20 +506,35 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
         // Codes come to shared memory three items ahead (each thread's own pieces, so that only its own copies are
         // waited for) and are converted (exactly) to halves on their way into the ring.  With one item ahead,
         // in registers, a tile pair took 3.0 us; like this 2.5 us (16-bit caches: 1.54).
-        constexpr int kRaw = Smem<D, FP8>::kRaw;
+        // E2M1: passes of KPP of the warp's 32 keys, a lane takes chunk cp of its kp-th; and one key's block scales, which
+        // the multiplications by them (exact, too) read from any lane's key of the warp.
+        constexpr int kRaw = Smem<D, KV>::kRaw, KPP = 32 / CPR;
+        [[maybe_unused]] const int kp = lane % KPP, cp = lane / KPP;
         int sent = 0;   // items whose copies are under way
         auto send = [&]() {
             if (sent < 2 * n) {
                 tell_gone(item + sent);
                 const uint8_t *base = sent & 1 ? c.v : c.k;
                 uint8_t *dst = sm.raw[sent % kRaw] + tid * 16;
+                if constexpr (KV == kKvE2M1) {
 #pragma unroll
-                for (int a = 0; a < GR; a++) {
-                    const int gi = w + 4 * a;
-                    const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi));
+                    for (int a = 0; a < CPR; a++) {
+                        const int key = a * KPP + kp, gi = w + 4 * (key >> 3);
+                        const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi), key & 7, 0, RB);
+                        cp_async16(dst + a * (kLoaders * 16), src ? src + cp * 16 : c.k, src ? 16 : 0);
+                    }
+                    const int gi = w + 4 * (lane >> 3);
+                    const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi), r8, (size_t)c.ps * RB, SB);
+                    cp_async_small<SB>(sm.raw_scale[sent % kRaw] + tid * SB, src ? src : c.k, src ? SB : 0);
+                } else {
 #pragma unroll
-                    for (int x = 0; x < PASS; x++)
-                        cp_async16(dst + (a * PASS + x) * (kLoaders * 16), src ? src + (x * 4 + q4) * 16 : c.k, src ? 16 : 0);
+                    for (int a = 0; a < GR; a++) {
+                        const int gi = w + 4 * a;
+                        const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi), r8, 0, RB);
+#pragma unroll
+                        for (int x = 0; x < PASS; x++)
+                            cp_async16(dst + (a * PASS + x) * (kLoaders * 16), src ? src + (x * 4 + q4) * 16 : c.k, src ? 16 : 0);
+                    }
                 }
                 if (sent & 1) {
                     pages = pages_next;
@@ -526,22 +549,44 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
             const uint32_t ring = item + it;
             const int slot = ring % kSlots;
             cp_async_wait<kRaw - 1>();
+            if constexpr (KV == kKvE2M1) __syncwarp();   // the block scales of the warp's keys, which its other lanes fetched
             if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
             const uint4 *src = reinterpret_cast<const uint4 *>(sm.raw[it % kRaw]) + tid;
+            if constexpr (KV == kKvE2M1) {
+                const uint8_t *scales = sm.raw_scale[it % kRaw] + w * 32 * SB;
 #pragma unroll
-            for (int a = 0; a < GR; a++)
-#pragma unroll
-                for (int x = 0; x < PASS; x++) {
-                    const uint4 v = src[(a * PASS + x) * kLoaders];
+                for (int a = 0; a < CPR; a++) {   // 32 codes, two blocks
+                    const int key = a * KPP + kp;
+                    const uint4 v = src[a * kLoaders];
                     const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t e[8];
+                    const uint32_t s2 = e4m3x2_half2(*reinterpret_cast<const uint16_t *>(scales + key * SB + 2 * cp));
+                    const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+                    const int row = (w + 4 * (key >> 3)) * 8 + (key & 7);
 #pragma unroll
-                    for (int s = 0; s < 4; s++) e4m3x4_half4(ws[s], e[2 * s], e[2 * s + 1]);
-#pragma unroll
-                    for (int s = 0; s < 2; s++)
-                        *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at((w + 4 * a) * 8 + r8, (x * 4 + q4) * 2 + s)) =
-                            make_uint4(e[4 * s], e[4 * s + 1], e[4 * s + 2], e[4 * s + 3]);
+                    for (int y = 0; y < 4; y++) {
+                        uint32_t e[4];
+                        e2m1x8_half8(ws[y], e);
+                        *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at(row, cp * 4 + y)) =
+                            make_uint4(hmul2(e[0], s[y >> 1]), hmul2(e[1], s[y >> 1]), hmul2(e[2], s[y >> 1]), hmul2(e[3], s[y >> 1]));
+                    }
                 }
+                __syncwarp();   // read by all lanes before the next fetch
+            } else {
+#pragma unroll
+                for (int a = 0; a < GR; a++)
+#pragma unroll
+                    for (int x = 0; x < PASS; x++) {
+                        const uint4 v = src[(a * PASS + x) * kLoaders];
+                        const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t e[8];
+#pragma unroll
+                        for (int s = 0; s < 4; s++) e4m3x4_half4(ws[s], e[2 * s], e[2 * s + 1]);
+#pragma unroll
+                        for (int s = 0; s < 2; s++)
+                            *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at((w + 4 * a) * 8 + r8, (x * 4 + q4) * 2 + s)) =
+                                make_uint4(e[4 * s], e[4 * s + 1], e[4 * s + 2], e[4 * s + 3]);
+                    }
+            }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.full[slot]);
             send();
@@ -553,15 +598,15 @@ __device__ bool load_unit(Smem<D, FP8> &sm, const Args &args, const Unit &u, int
     return true;
 }
 
-template <int D, typename Q, bool FP8>
-__device__ void load_role(Smem<D, FP8> &sm, const Args &args, int W, int S)
+template <int D, typename Q, int KV>
+__device__ void load_role(Smem<D, KV> &sm, const Args &args, int W, int S)
 {
-    constexpr uint32_t kSlots = Smem<D, FP8>::kSlots;
+    constexpr uint32_t kSlots = Smem<D, KV>::kSlots;
     uint32_t item = 0, units = 0;
     for (int k = 0; const Unit *at = unit_of(sm, k, args.p.c.err); k++) {
         const Unit u = *at;
         unit_done(sm, k);
-        if (u.tb > u.ta && !load_unit<D, Q, FP8>(sm, args, u, W, S, item, units)) break;
+        if (u.tb > u.ta && !load_unit<D, Q, KV>(sm, args, u, W, S, item, units)) break;
     }
     cp_async_wait<0>();
     // where a wait gave up, tiles may still be landing: let them (the last one of each slot)
@@ -598,7 +643,7 @@ __device__ __forceinline__ void store_row(uint16_t *dst, bool wide, const float 
 __device__ __forceinline__ bool wide_stores(const AttnParams &p) { return (reinterpret_cast<uintptr_t>(p.out) & 31) == 0; }
 
 // One row of a split unit from its pieces; `at`: the first piece's m of this row
-template <int D, typename Q, bool FP8>
+template <int D, typename Q, int KV>
 __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const float *at)
 {
     const size_t row = row_index(p, u, threadIdx.x);
@@ -608,7 +653,7 @@ __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const 
     for (int i = 0; i < u.pieces; i++) m = fmaxf(m, __ldcg(at + i * step));
     const float base = m == -INFINITY ? 0.f : m;
     for (int i = 0; i < u.pieces; i++) l += ex2(__ldcg(at + i * step) - base) * __ldcg(at + i * step + kRowsCta);
-    const float f = l == 0.f ? 0.f : (FP8 ? p.c.v_scale[p.layer * p.c.Hkv + u.h] : 1.f) / l;
+    const float f = l == 0.f ? 0.f : (KV != kKv16 ? p.c.v_scale[p.layer * p.c.Hkv + u.h] : 1.f) / l;
     for (int d = 0; d < D; d += 32) {
         float o[32];
 #pragma unroll
@@ -625,24 +670,25 @@ __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const 
 
 // ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far; `all_units`:
 // those of either half, `all_tiles`: their key tiles)
-template <int D, typename Q, bool FP8>
-__device__ bool softmax_unit(Smem<D, FP8> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
+template <int D, typename Q, int KV>
+__device__ bool softmax_unit(Smem<D, KV> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
                              uint32_t &tiles, uint32_t &units, uint32_t all_units, uint32_t all_tiles)
 {
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, h = tid >> 7, rl = tid & 127, w = tid >> 5;
     const int n = u.tb - u.ta;
+    constexpr bool CODES = KV != kKv16;
     const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
     const int x = h * kHalf + rl;                                // row of the unit
     const bool live = x < u.rows;
-    using P = std::conditional_t<FP8, Half, Q>;                  // type of the products
+    using P = std::conditional_t<CODES, Half, Q>;                  // type of the products
     float row_scale = 1.f;
-    if constexpr (FP8 && !Q::is_half) {
+    if constexpr (CODES && !Q::is_half) {
         // (the barrier of this parity cannot move on again before this half's last scores of the unit are read)
         if (!wait_warp(sm, &sm.q_full[all_units & 1], (all_units >> 1) & 1, c.err)) return false;
         row_scale = sm.q_scale[all_units & 1][x];
     }
-    const float sc = score_scale(p.scale_log2 * (FP8 ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f) * row_scale);
+    const float sc = score_scale(p.scale_log2 * (CODES ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f) * row_scale);
     const int first = u.len - u.n;
     const int pos = first + row_token(p, u, min(x, u.rows - 1));  // this row's position
     const int lo = (int)max(-0x7fffffffll, (long long)pos - W + 1);
@@ -724,7 +770,7 @@ __device__ bool softmax_unit(Smem<D, FP8> &sm, const AttnParams &p, const Unit &
     tc::fence_after_sync();
     tiles += n;
     units++;
-    const float f = l == 0.f ? 0.f : (FP8 ? c.v_scale[p.layer * c.Hkv + u.h] : 1.f) / l;
+    const float f = l == 0.f ? 0.f : (CODES ? c.v_scale[p.layer * c.Hkv + u.h] : 1.f) / l;
     const size_t row = row_index(p, u, x);
     uint16_t *dst = p.out + row * D;
     const bool wide = wide_stores(p);
@@ -757,8 +803,8 @@ __device__ __forceinline__ bool softmax_sync(SM &sm, uint32_t &joins, int *err)
     return wait_warp(sm, &sm.join, joins++ & 1, err);
 }
 
-template <int D, typename Q, bool FP8>
-__device__ void softmax_role(Smem<D, FP8> &sm, const AttnParams &p, uint32_t tmem, int W, int S)
+template <int D, typename Q, int KV>
+__device__ void softmax_role(Smem<D, KV> &sm, const AttnParams &p, uint32_t tmem, int W, int S)
 {
     const int tid = threadIdx.x, h = tid >> 7;
     int *count = reinterpret_cast<int *>(p.ws);
@@ -776,7 +822,7 @@ __device__ void softmax_role(Smem<D, FP8> &sm, const AttnParams &p, uint32_t tme
                 if (p.lse) p.lse[row] = -INFINITY;
             }
         } else {
-            if (h < u.halves && !softmax_unit<D, Q, FP8>(sm, p, u, tmem, W, S, partial, tiles, units, all_units, all_tiles)) return;
+            if (h < u.halves && !softmax_unit<D, Q, KV>(sm, p, u, tmem, W, S, partial, tiles, units, all_units, all_tiles)) return;
             all_units++;
             all_tiles += u.tb - u.ta;
             if (partial) {
@@ -790,7 +836,7 @@ __device__ void softmax_role(Smem<D, FP8> &sm, const AttnParams &p, uint32_t tme
                     __threadfence();
                 }
                 if (!softmax_sync(sm, joins, p.c.err)) return;
-                if (sm.last && tid < u.rows) join_row<D, Q, FP8>(p, u, ws.slot(u.first, D) + tid);
+                if (sm.last && tid < u.rows) join_row<D, Q, KV>(p, u, ws.slot(u.first, D) + tid);
                 if (!softmax_sync(sm, joins, p.c.err)) return;   // sm.last is read
             }
         }
@@ -931,12 +977,12 @@ __device__ void unit_role(SM &sm, const AttnParams &p, int W, int S)
     if (lane == 0 && atomicAdd(counter + 1, 1) == (int)gridDim.x - 1) counter[0] = counter[1] = 0;
 }
 
-template <int D, typename Q, bool FP8>
+template <int D, typename Q, int KV>
 __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __grid_constant__ Args args)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // the swizzle repeats every 1024 bytes of the shared address
-    Smem<D, FP8> &sm = *reinterpret_cast<Smem<D, FP8> *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    Smem<D, KV> &sm = *reinterpret_cast<Smem<D, KV> *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const AttnParams &p = args.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
@@ -945,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.join, kSoftmax / 32);
         mbar_init(&sm.drain, 1);
-        for (int i = 0; i < (int)Smem<D, FP8>::kSlots; i++) {
+        for (int i = 0; i < (int)Smem<D, KV>::kSlots; i++) {
             mbar_init(&sm.full[i], kLoaders);
             mbar_init(&sm.empty[i], 1);
         }
@@ -997,17 +1043,17 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
     const uint32_t tmem = sm.tmem;
     if (warp < 8) {
         regs_inc<kRegsSoftmax>();
-        softmax_role<D, Q, FP8>(sm, p, tmem, W, S);
+        softmax_role<D, Q, KV>(sm, p, tmem, W, S);
         __syncwarp();
         regs_dec<kRegs>();   // back to what the common code was compiled for
     } else if (warp < 12) {
         regs_dec<kRegsLoad>();
-        load_role<D, Q, FP8>(sm, args, W, S);
+        load_role<D, Q, KV>(sm, args, W, S);
         __syncwarp();
         regs_inc<kRegs>();
     } else {
         regs_dec<kRegsMma>();
-        if (warp == 12) mma_role<D, std::conditional_t<FP8, Half, Q>>(sm, __reduce_max_sync(~0u, tmem), p.c.err);
+        if (warp == 12) mma_role<D, std::conditional_t<KV != kKv16, Half, Q>>(sm, __reduce_max_sync(~0u, tmem), p.c.err);
         else if (warp == 13) unit_role(sm, p, W, S);
         __syncwarp();
         regs_inc<kRegs>();
@@ -1075,12 +1121,12 @@ bool map_queries(CUtensorMap *map, const AttnParams &p)
                   {64, (cuuint32_t)p.G, (cuuint32_t)(kHalf / p.G)}) == cudaSuccess;
 }
 
-template <int D, typename Q, bool FP8>
+template <int D, typename Q, int KV>
 cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
 {
     static KernelSetup setup;
-    constexpr size_t smem = sizeof(Smem<D, FP8>) + 1024;
-    cudaError_t e = setup.get(kda_attn_prefill_kernel<D, Q, FP8>, kThreads, smem, 0, nullptr);
+    constexpr size_t smem = sizeof(Smem<D, KV>) + 1024;
+    cudaError_t e = setup.get(kda_attn_prefill_kernel<D, Q, KV>, kThreads, smem, 0, nullptr);
     if (e != cudaSuccess) return e;
     int sms = 0;
     if ((e = paged_sm_count(&sms)) != cudaSuccess) return e;
@@ -1091,27 +1137,33 @@ cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
     if (units > 0x7fffffffll) return cudaErrorInvalidValue;
     Args a = {};
     a.p = p;
-    if (!FP8 && ((e = encode_pages(&a.k, p.c.k, p.c)) != cudaSuccess || (e = encode_pages(&a.v, p.c.v, p.c)) != cudaSuccess)) return e;
+    if (KV == kKv16 && ((e = encode_pages(&a.k, p.c.k, p.c)) != cudaSuccess || (e = encode_pages(&a.v, p.c.v, p.c)) != cudaSuccess)) return e;
     a.q_map = map_queries(&a.q, p);
     a.p.inv_g = 1.f / p.G;
     const int ctas = sms < kMaxSplitCtas ? sms : kMaxSplitCtas;
-    return launch_pdl(kda_attn_prefill_kernel<D, Q, FP8>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a);
+    return launch_pdl(kda_attn_prefill_kernel<D, Q, KV>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a);
 }
 
-template <int D>
-cudaError_t launch_types(const AttnParams &p, cudaStream_t stream)
+template <int KV>
+cudaError_t launch_kind(const AttnParams &p, cudaStream_t stream)
 {
-    if (p.c.dtype == KDA_T_E4M3) return p.f16 ? launch_as<D, Half, true>(p, stream) : launch_as<D, Bf16, true>(p, stream);
-    return p.f16 ? launch_as<D, Half, false>(p, stream) : launch_as<D, Bf16, false>(p, stream);
+    if (p.c.D == 128) return p.f16 ? launch_as<128, Half, KV>(p, stream) : launch_as<128, Bf16, KV>(p, stream);
+    return p.f16 ? launch_as<64, Half, KV>(p, stream) : launch_as<64, Bf16, KV>(p, stream);
 }
 
 }  // namespace
 
+#ifdef KDA_PREFILL_E2M1   // a translation unit of its own (kda_attn_prefill_e2m1.cu), compiled beside the other's
+cudaError_t launch_attn_prefill_e2m1(const AttnParams &p, cudaStream_t stream) { return launch_kind<kKvE2M1>(p, stream); }
+#else
 size_t attn_prefill_workspace(int D) { return kAttnCounters * sizeof(int) + kMaxSplitCtas * SplitWs::slot_floats(D) * sizeof(float); }
 
 cudaError_t launch_attn_prefill(const AttnParams &p, cudaStream_t stream)
 {
-    return p.c.D == 128 ? launch_types<128>(p, stream) : launch_types<64>(p, stream);
+    return p.c.dtype == KDA_T_E2M1   ? launch_attn_prefill_e2m1(p, stream)
+           : p.c.dtype == KDA_T_E4M3 ? launch_kind<kKvE4M3>(p, stream)
+                                     : launch_kind<kKv16>(p, stream);
 }
+#endif
 
 }  // namespace kda

@@ -7,7 +7,7 @@
 #include <cooperative_groups.h>
 
 #include "kda_paged.cuh"
-#include "kda_tc.cuh"
+#include "kda_quant.cuh"
 
 namespace kda {
 namespace {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256) kda_kv_copy_tails_kernel(const KvCall p)
     const Scratch s(p);
     grid_dependency_wait();
     const int n = s.meta[0], lane = threadIdx.x & 31;
-    const size_t row = (size_t)c.D * c.elem(), head = row * c.ps;
+    const size_t row = (size_t)c.token_bytes(), head = row * c.ps;
     const int pieces = (int)((head + kTail - 1) / kTail);
     const long long items = (long long)n * c.layers * 2 * c.Hkv * pieces;
     for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (long long)gridDim.x * 8) {
@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(256) kda_kv_copy_tails_kernel(const KvCall p)
         const int kv = (int)(x & 1);
         x >>= 1;
         const int layer = (int)(x % c.layers), i = (int)(x / c.layers);
-        const int chunks = (int)(s.cow_n[i] * row) / 16 - piece * (kTail / 16);   // left from this piece on
+        const int tokens = c.dtype == KDA_T_E2M1 ? c.ps : s.cow_n[i];   // a 4-bit head's codes and scales stand apart: all of it
+        const int chunks = (int)(tokens * row) / 16 - piece * (kTail / 16);   // left from this piece on
         uint8_t *base = (kv ? c.v : c.k) + (size_t)layer * c.pages * c.page_bytes() + h * head + (size_t)piece * kTail;
         const uint4 *src = reinterpret_cast<const uint4 *>(base + (size_t)s.cow_src[i] * c.page_bytes());
         uint4 *dst = reinterpret_cast<uint4 *>(base + (size_t)s.cow_dst[i] * c.page_bytes());
@@ -453,39 +454,9 @@ __device__ __forceinline__ void append_piece(const uint4 w, uint8_t *dst, float2
             g[2 * i] = v.x;
             g[2 * i + 1] = v.y;
         }
-        // The code is the rounding of the IEEE quotient.  Markstein's theorem gives that quotient from the correctly
-        // rounded reciprocal: q = f r, then q + (f - q scale) r, three packed operations for two elements
-        // (a division each took 57 us for 33000 tokens, bound by its instructions); with f = -g as q - (q scale + g) r,
-        // whose inner sum is +0 where q is exact, so that a zero keeps its sign.  Infinities, and scales whose
-        // reciprocal or products could leave the normal range (their reciprocal is given as NaN), take the
-        // division.
-        float t0 = 0.f, t1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float e0, e1;
-            tc::mul2(q[i], q[i + 1], g[i], g[i + 1], -scale.y, -scale.y);
-            tc::fma2(e0, e1, q[i], q[i + 1], scale.x, scale.x, g[i], g[i + 1]);
-            tc::fma2(q[i], q[i + 1], e0, e1, -scale.y, -scale.y, q[i], q[i + 1]);
-            tc::add2(t0, t1, t0, t1, q[i], q[i + 1]);
-        }
-        if (!(fabsf(t0 + t1) < 1e30f)) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) q[i] = __fdiv_rn(-g[i], scale.x);
-        }
-        uint32_t o[2];
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-            o[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * i], q[4 * i + 1]), __NV_SATFINITE, __NV_E4M3) |
-                   (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * i + 2], q[4 * i + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(o[0], o[1]);
+        neg_quotients8(g, scale, q);
+        *reinterpret_cast<uint2 *>(dst) = e4m3x8(q);
     }
-}
-
-// A scale and its correctly rounded reciprocal, NaN where quotients cannot be had from it.
-__device__ __forceinline__ float2 with_reciprocal(float scale)
-{
-    const float a = fabsf(scale);
-    return make_float2(scale, a > 1e-18f && a < 1e18f ? __frcp_rn(scale) : NAN);
 }
 
 template <bool E4M3, bool F16>
@@ -523,45 +494,8 @@ __global__ void __launch_bounds__(256) kda_kv_append_kernel(const AppendParams p
         __syncthreads();
     }
     if (tok >= tokens) return;
-    int b, t, n;
-    if (p.cu) {
-        // the sequence whose offsets hold this row: the last b with cu[b] <= tok, 32 at a time
-        int a = 0, e = p.B;   // in [a, e)
-        while (e - a > 1) {
-            const int step = (e - a + 31) / 32;
-            const int at = a + lane * step;
-            const bool le = at < e && p.cu[at] <= tok;
-            const unsigned m = __ballot_sync(~0u, le);
-            const int k = m ? 31 - __clz(m) : 0;
-            a += k * step;
-            e = min(e, a + step);
-        }
-        b = a;
-        const int c0 = p.cu[b], c1 = p.cu[b + 1];
-        if (c0 < 0 || c1 < c0 || c1 > p.T) {
-            if (lane == 0) atomicOr(c.err, KDA_DEVERR_SEQLEN);
-            return;
-        }
-        if (tok < c0 || tok >= c1) return;   // rows outside every sequence
-        t = (int)(tok - c0);
-        n = c1 - c0;
-    } else {
-        b = (int)seq;
-        t = (int)in_seq;
-        n = p.n_tokens ? p.n_tokens[b] : p.T;
-    }
-    const SeqInfo s = seq_info(c, p.rows[b], n, p.cu ? 0x7fffffff : p.T, t == 0 && lane == 0);
-    if (!s.ok || t >= n) return;
-    if (n > s.len) {   // fewer tokens in the row than the call brings
-        if (lane == 0) atomicOr(c.err, KDA_DEVERR_SEQLEN);
-        return;
-    }
-    const int pos = s.len - n + t;
-    const int page = c.table[(size_t)s.row * c.width + (pos >> c.ps_log2)];
-    if ((unsigned)page >= (unsigned)c.pages) {
-        if (lane == 0) atomicOr(c.err, KDA_DEVERR_PAGE);
-        return;
-    }
+    int pos, page;
+    if (!append_place(p, tok, seq, in_seq, lane, lane == 0, pos, page)) return;
     constexpr int ES = E4M3 ? 1 : 2;
     const size_t row = (size_t)c.D * ES, head = row * c.ps;
     const size_t at = ((size_t)p.layer * c.pages + page) * c.page_bytes() + (pos & (c.ps - 1)) * row;

@@ -19,9 +19,10 @@ struct PagedCache {
     int *table, *lens, *refs;
     const float *k_scale, *v_scale;
     int *err;
-    __host__ __device__ int elem() const { return dtype == KDA_T_E4M3 ? 1 : 2; }
+    // bytes of one token of one head (E2M1: its codes and block scales, which stand apart, see kda_kv_cache)
+    __host__ __device__ int token_bytes() const { return dtype == KDA_T_E2M1 ? D / 2 + D / 16 : dtype == KDA_T_E4M3 ? D : 2 * D; }
     // bytes of one page of one layer, all heads
-    __host__ __device__ size_t page_bytes() const { return (size_t)Hkv * ps * D * elem(); }
+    __host__ __device__ size_t page_bytes() const { return (size_t)Hkv * ps * token_bytes(); }
 };
 
 struct KvCall {
@@ -55,6 +56,39 @@ struct AppendParams {
 };
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
 
+// How positions turn the pairs of a head (kda_rope_desc).
+struct Turns {
+    const unsigned long long *freq;   // [rot / 2] turns per position, in units of 2^-64
+    int rot, adjacent;
+    float scale;
+};
+// A tensor whose heads are turned on their way from src to dst.
+struct TurnedTensor {
+    const uint16_t *src;
+    uint16_t *dst;
+    int heads;
+    TokensLayout sl, dl;
+};
+struct RopeParams {
+    Turns r;
+    const int *pos;                // [tokens]
+    int tokens, T, D;              // T: tokens per sequence
+    int lanes_log2;                // lanes of a head, parts: warps of a token (set by the launcher)
+    int parts;
+    TurnedTensor x[2];
+    bool f16;
+};
+cudaError_t launch_rope(RopeParams p, cudaStream_t stream);
+
+// An append whose keys (and the queries `q`, where it has heads) are turned, or one to a 4-bit cache.
+struct AppendTurnParams {
+    AppendParams a;
+    Turns r;                       // freq null: nothing is turned
+    TurnedTensor q;
+    int parts;
+};
+cudaError_t launch_kv_append_turn(AppendTurnParams p, cudaStream_t stream);
+
 struct AttnParams {
     PagedCache c;
     int layer, Hq, G;
@@ -76,7 +110,10 @@ struct AttnParams {
 constexpr size_t kAttnCounters = 4096;
 cudaError_t launch_attn_decode64(const AttnParams &p, cudaStream_t stream);
 cudaError_t launch_attn_decode128(const AttnParams &p, cudaStream_t stream);
+cudaError_t launch_attn_decode64_e2m1(const AttnParams &p, cudaStream_t stream);
+cudaError_t launch_attn_decode128_e2m1(const AttnParams &p, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const AttnParams &p, cudaStream_t stream);
+cudaError_t launch_attn_prefill_e2m1(const AttnParams &p, cudaStream_t stream);
 size_t attn_decode_workspace(int D);
 size_t attn_prefill_workspace(int D);
 
@@ -140,6 +177,54 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedCache &c, int row, int n,
     s.ok = err == 0;
     if (err && report) atomicOr(c.err, err);
     return s;
+}
+
+// Position, and page, of token `tok` of an append (token in_seq of sequence seq without offsets), looked up by a whole warp;
+// false where it has none (`say` is the thread that sets the error word then).
+__device__ __forceinline__ bool append_place(const AppendParams &p, long long tok, long long seq, long long in_seq, int lane, bool say,
+                                             int &pos, int &page)
+{
+    const PagedCache &c = p.c;
+    int b, t, n;
+    if (p.cu) {
+        // the sequence whose offsets hold this row: the last b with cu[b] <= tok, 32 at a time
+        int a = 0, e = p.B;   // in [a, e)
+        while (e - a > 1) {
+            const int step = (e - a + 31) / 32;
+            const int at = a + lane * step;
+            const bool le = at < e && p.cu[at] <= tok;
+            const unsigned m = __ballot_sync(~0u, le);
+            const int k = m ? 31 - __clz(m) : 0;
+            a += k * step;
+            e = min(e, a + step);
+        }
+        b = a;
+        const int c0 = p.cu[b], c1 = p.cu[b + 1];
+        if (c0 < 0 || c1 < c0 || c1 > p.T) {
+            if (say) atomicOr(c.err, KDA_DEVERR_SEQLEN);
+            return false;
+        }
+        if (tok < c0 || tok >= c1) return false;   // rows outside every sequence
+        t = (int)(tok - c0);
+        n = c1 - c0;
+    } else {
+        b = (int)seq;
+        t = (int)in_seq;
+        n = p.n_tokens ? p.n_tokens[b] : p.T;
+    }
+    const SeqInfo s = seq_info(c, p.rows[b], n, p.cu ? 0x7fffffff : p.T, t == 0 && say);
+    if (!s.ok || t >= n) return false;
+    if (n > s.len) {   // fewer tokens in the row than the call brings
+        if (say) atomicOr(c.err, KDA_DEVERR_SEQLEN);
+        return false;
+    }
+    pos = s.len - n + t;
+    page = c.table[(size_t)s.row * c.width + (pos >> c.ps_log2)];
+    if ((unsigned)page >= (unsigned)c.pages) {
+        if (say) atomicOr(c.err, KDA_DEVERR_PAGE);
+        return false;
+    }
+    return true;
 }
 
 }  // namespace kda

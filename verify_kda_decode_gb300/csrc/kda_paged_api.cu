@@ -42,11 +42,13 @@ bool aligned(const void *p, uintptr_t n) { return p != nullptr && (reinterpret_c
         if (s_ != KDA_OK) return s_;         \
     } while (0)
 
+bool of_codes(const kda_kv_cache *cache) { return cache->kv_dtype == KDA_T_E4M3 || cache->kv_dtype == KDA_T_E2M1; }
+
 kda_status check_cache(const kda_kv_cache *cache)
 {
     if (!cache) return fail(KDA_ERR_INVALID_ARG, "cache is null");
-    if (cache->kv_dtype != KDA_T_BF16 && cache->kv_dtype != KDA_T_F16 && cache->kv_dtype != KDA_T_E4M3)
-        return fail(KDA_ERR_INVALID_ARG, "kv_dtype=%d is none of KDA_T_BF16, KDA_T_F16, KDA_T_E4M3", cache->kv_dtype);
+    if (cache->kv_dtype != KDA_T_BF16 && cache->kv_dtype != KDA_T_F16 && !of_codes(cache))
+        return fail(KDA_ERR_INVALID_ARG, "kv_dtype=%d is none of KDA_T_BF16, KDA_T_F16, KDA_T_E4M3, KDA_T_E2M1", cache->kv_dtype);
     if (cache->num_layers < 1 || cache->num_pages < 1 || cache->num_kv_heads < 1 || cache->rows < 1 || cache->max_pages < 1)
         return fail(KDA_ERR_INVALID_ARG, "num_layers=%d, num_pages=%d, num_kv_heads=%d, rows=%d, max_pages=%d: each must be >= 1",
                     cache->num_layers, cache->num_pages, cache->num_kv_heads, cache->rows, cache->max_pages);
@@ -67,7 +69,7 @@ kda_status check_cache(const kda_kv_cache *cache)
     NEED(cache->seq_lens, 4);
     NEED(cache->page_refs, 4);
     NEED(cache->err_word, 4);
-    if (cache->kv_dtype == KDA_T_E4M3) {
+    if (of_codes(cache)) {
         NEED(cache->k_scale, 4);
         NEED(cache->v_scale, 4);
     }
@@ -120,13 +122,13 @@ kda_status check_layer_index(const kda_kv_cache *cache, int32_t layer)
     return KDA_OK;
 }
 
-// Layout of [seq, token, head, D] elements, D contiguous, read 16 bytes at a time.
+// Layout of [seq, token, head, D] elements, D contiguous, read 16 bytes at a time; `cache`: what has to hold them, or null.
 kda_status check_layout(const kda_kv_cache *cache, const kda_tokens_layout *l, const char *name)
 {
     if (!l) return fail(KDA_ERR_INVALID_ARG, "layout of %s is null", name);
     if (l->dtype != KDA_T_BF16 && l->dtype != KDA_T_F16)
         return fail(KDA_ERR_INVALID_ARG, "%s: dtype=%d is neither KDA_T_BF16 nor KDA_T_F16", name, l->dtype);
-    if (cache->kv_dtype != KDA_T_E4M3 && l->dtype != cache->kv_dtype)
+    if (cache && !of_codes(cache) && l->dtype != cache->kv_dtype)
         return fail(KDA_ERR_INVALID_ARG, "%s: dtype=%d, the cache holds %d", name, l->dtype, cache->kv_dtype);
     if (l->seq_stride < 0 || l->token_stride < 0 || l->head_stride < 0) return fail(KDA_ERR_INVALID_ARG, "%s: negative stride", name);
     if ((l->seq_stride | l->token_stride | l->head_stride) & 7)
@@ -181,6 +183,83 @@ kda::AttnParams attn_params(const kda_kv_cache *cache, int32_t layer, const kda_
     p.f16 = desc->q.dtype == KDA_T_F16;
     p.ws = static_cast<uint8_t *>(workspace);
     return p;
+}
+
+kda_status check_append(const kda_kv_cache *cache, int32_t layer, int32_t B, int32_t T, const int32_t *n_tokens, const int32_t *cu_seqlens,
+                        const kda_tokens_layout *k_layout, const kda_tokens_layout *v_layout)
+{
+    CHECK(check_cache(cache));
+    CHECK(check_layer_index(cache, layer));
+    if (B < 0 || T < 0) return fail(KDA_ERR_INVALID_ARG, "B=%d, T=%d: each must be >= 0", B, T);
+    CHECK(check_layout(cache, k_layout, "k"));
+    CHECK(check_layout(cache, v_layout, "v"));
+    if (k_layout->dtype != v_layout->dtype) return fail(KDA_ERR_INVALID_ARG, "k and v have different types");
+    if (n_tokens && cu_seqlens) return fail(KDA_ERR_INVALID_ARG, "n_tokens and cu_seqlens exclude each other");
+    if (!cu_seqlens && (long long)B * T > 0x7fffffffll) return fail(KDA_ERR_UNSUPPORTED, "B * T = %lld does not fit 31 bits", (long long)B * T);
+    return KDA_OK;
+}
+
+kda_status check_append_pointers(const int32_t *rows, const int32_t *n_tokens, const int32_t *cu_seqlens, const void *k, const void *v)
+{
+    NEED(rows, 4);
+    if (n_tokens) NEED(n_tokens, 4);
+    if (cu_seqlens) NEED(cu_seqlens, 4);
+    NEED(k, 16);
+    NEED(v, 16);
+    return KDA_OK;
+}
+
+kda::AppendParams append_params(const kda_kv_cache *cache, int32_t layer, const int32_t *rows, int32_t B, int32_t T, const int32_t *n_tokens,
+                                const int32_t *cu_seqlens, const void *k, const kda_tokens_layout *k_layout, const void *v, const kda_tokens_layout *v_layout)
+{
+    kda::AppendParams p;
+    memset(&p, 0, sizeof p);
+    p.c = paged(cache);
+    p.layer = layer;
+    p.rows = rows;
+    p.n_tokens = n_tokens;
+    p.cu = cu_seqlens;
+    p.B = B;
+    p.T = T;
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.kl = layout(k_layout);
+    p.vl = layout(v_layout);
+    p.f16 = k_layout->dtype == KDA_T_F16;
+    return p;
+}
+
+kda_status check_rope(const kda_rope_desc *rope, int32_t head_dim)
+{
+    if (!rope) return fail(KDA_ERR_INVALID_ARG, "rope is null");
+    if (rope->rotary_dim < 16 || rope->rotary_dim > head_dim || rope->rotary_dim % 16)
+        return fail(KDA_ERR_UNSUPPORTED, "rotary_dim=%d is no multiple of 16 from 16 to head_dim=%d", rope->rotary_dim, head_dim);
+    if (rope->interleaved != 0 && rope->interleaved != 1) return fail(KDA_ERR_INVALID_ARG, "interleaved=%d is neither 0 nor 1", rope->interleaved);
+    if (!isfinite(rope->scale)) return fail(KDA_ERR_INVALID_ARG, "rope: scale must be finite");
+    return KDA_OK;
+}
+
+// `x` over B sequences of T tokens; tokens and heads of the turned copy are apart.
+kda_status check_turned(const kda_kv_cache *cache, const kda_rope_layout *x, const char *name, int32_t B, int32_t T)
+{
+    if (!x) return fail(KDA_ERR_INVALID_ARG, "layout of %s is null", name);
+    if (x->num_heads < 1 || x->num_heads > 65536) return fail(KDA_ERR_INVALID_ARG, "%s: num_heads=%d outside [1, 65536]", name, x->num_heads);
+    CHECK(check_layout(cache, &x->src, name));
+    CHECK(check_layout(cache, &x->dst, name));
+    if (x->src.dtype != x->dst.dtype) return fail(KDA_ERR_INVALID_ARG, "%s and %s_out have different types", name, name);
+    if ((x->num_heads > 1 && x->dst.head_stride == 0) || (T > 1 && x->dst.token_stride == 0) || (B > 1 && x->dst.seq_stride == 0))
+        return fail(KDA_ERR_INVALID_ARG, "%s_out: its heads or tokens share memory", name);
+    return KDA_OK;
+}
+
+kda::Turns turns(const kda_rope_desc *rope)
+{
+    return {reinterpret_cast<const unsigned long long *>(rope->turns), rope->rotary_dim, rope->interleaved, rope->scale};
+}
+
+kda::TurnedTensor turned(const kda_rope_layout *x, const void *src, void *dst)
+{
+    return {static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), x->num_heads, layout(&x->src), layout(&x->dst)};
 }
 
 kda::KvCall kv_call(const kda_kv_cache *cache, const int32_t *rows, const int32_t *arg, int32_t B, void *workspace)
@@ -258,35 +337,77 @@ kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t
                          const int32_t *n_tokens, const int32_t *cu_seqlens, const void *k,
                          const kda_tokens_layout *k_layout, const void *v, const kda_tokens_layout *v_layout, void *stream)
 {
-    CHECK(check_cache(cache));
-    CHECK(check_layer_index(cache, layer));
-    if (B < 0 || T < 0) return fail(KDA_ERR_INVALID_ARG, "B=%d, T=%d: each must be >= 0", B, T);
-    CHECK(check_layout(cache, k_layout, "k"));
-    CHECK(check_layout(cache, v_layout, "v"));
-    if (k_layout->dtype != v_layout->dtype) return fail(KDA_ERR_INVALID_ARG, "k and v have different types");
-    if (n_tokens && cu_seqlens) return fail(KDA_ERR_INVALID_ARG, "n_tokens and cu_seqlens exclude each other");
-    if (!cu_seqlens && (long long)B * T > 0x7fffffffll) return fail(KDA_ERR_UNSUPPORTED, "B * T = %lld does not fit 31 bits", (long long)B * T);
+    CHECK(check_append(cache, layer, B, T, n_tokens, cu_seqlens, k_layout, v_layout));
     if (B == 0 || T == 0) return launched(cudaSuccess);
-    NEED(rows, 4);
-    if (n_tokens) NEED(n_tokens, 4);
-    if (cu_seqlens) NEED(cu_seqlens, 4);
-    NEED(k, 16);
-    NEED(v, 16);
-    kda::AppendParams p;
+    CHECK(check_append_pointers(rows, n_tokens, cu_seqlens, k, v));
+    const kda::AppendParams p = append_params(cache, layer, rows, B, T, n_tokens, cu_seqlens, k, k_layout, v, v_layout);
+    if (cache->kv_dtype != KDA_T_E2M1) return launched(kda::launch_kv_append(p, static_cast<cudaStream_t>(stream)));
+    kda::AppendTurnParams t;
+    memset(&t, 0, sizeof t);
+    t.a = p;
+    return launched(kda::launch_kv_append_turn(t, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_rope(const kda_rope_desc *rope, int32_t head_dim, const int32_t *positions, int32_t B, int32_t T,
+                    const kda_rope_layout *q_layout, const void *q, void *q_out, const kda_rope_layout *k_layout, const void *k,
+                    void *k_out, void *stream)
+{
+    if (head_dim < 16 || head_dim > 512 || head_dim % 16)
+        return fail(KDA_ERR_UNSUPPORTED, "head_dim=%d is no multiple of 16 from 16 to 512", head_dim);
+    CHECK(check_rope(rope, head_dim));
+    if (B < 0 || T < 0) return fail(KDA_ERR_INVALID_ARG, "B=%d, T=%d: each must be >= 0", B, T);
+    if ((long long)B * T > 0x7fffffffll) return fail(KDA_ERR_UNSUPPORTED, "B * T = %lld does not fit 31 bits", (long long)B * T);
+    CHECK(check_turned(nullptr, q_layout, "q", B, T));
+    if (k_layout) {
+        CHECK(check_turned(nullptr, k_layout, "k", B, T));
+        if (k_layout->src.dtype != q_layout->src.dtype) return fail(KDA_ERR_INVALID_ARG, "q and k have different types");
+    }
+    if (B == 0 || T == 0) return launched(cudaSuccess);
+    NEED(rope->turns, 8);
+    NEED(positions, 4);
+    NEED(q, 16);
+    NEED(q_out, 16);
+    kda::RopeParams p;
     memset(&p, 0, sizeof p);
-    p.c = paged(cache);
-    p.layer = layer;
-    p.rows = rows;
-    p.n_tokens = n_tokens;
-    p.cu = cu_seqlens;
-    p.B = B;
+    p.r = turns(rope);
+    p.pos = positions;
+    p.tokens = B * T;
     p.T = T;
-    p.k = static_cast<const uint16_t *>(k);
-    p.v = static_cast<const uint16_t *>(v);
-    p.kl = layout(k_layout);
-    p.vl = layout(v_layout);
-    p.f16 = k_layout->dtype == KDA_T_F16;
-    return launched(kda::launch_kv_append(p, static_cast<cudaStream_t>(stream)));
+    p.D = head_dim;
+    p.x[0] = turned(q_layout, q, q_out);
+    if (k_layout) {
+        NEED(k, 16);
+        NEED(k_out, 16);
+        p.x[1] = turned(k_layout, k, k_out);
+    }
+    p.f16 = q_layout->src.dtype == KDA_T_F16;
+    return launched(kda::launch_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_kv_append_rope(const kda_kv_cache *cache, int32_t layer, const kda_rope_desc *rope, const int32_t *rows,
+                              int32_t B, int32_t T, const int32_t *n_tokens, const int32_t *cu_seqlens,
+                              const kda_rope_layout *q_layout, const void *q, void *q_out, const void *k,
+                              const kda_tokens_layout *k_layout, const void *v, const kda_tokens_layout *v_layout, void *stream)
+{
+    CHECK(check_append(cache, layer, B, T, n_tokens, cu_seqlens, k_layout, v_layout));
+    CHECK(check_rope(rope, cache->head_dim));
+    if (q_layout) {
+        CHECK(check_turned(cache, q_layout, "q", cu_seqlens ? 1 : B, T));
+        if (q_layout->src.dtype != k_layout->dtype) return fail(KDA_ERR_INVALID_ARG, "q and k have different types");
+    }
+    if (B == 0 || T == 0) return launched(cudaSuccess);
+    CHECK(check_append_pointers(rows, n_tokens, cu_seqlens, k, v));
+    NEED(rope->turns, 8);
+    kda::AppendTurnParams t;
+    memset(&t, 0, sizeof t);
+    t.a = append_params(cache, layer, rows, B, T, n_tokens, cu_seqlens, k, k_layout, v, v_layout);
+    t.r = turns(rope);
+    if (q_layout) {
+        NEED(q, 16);
+        NEED(q_out, 16);
+        t.q = turned(q_layout, q, q_out);
+    }
+    return launched(kda::launch_kv_append_turn(t, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kda_attn_workspace_size(const kda_kv_cache *cache)

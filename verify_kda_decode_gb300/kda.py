@@ -25,7 +25,7 @@ KDA_W_BF16, KDA_W_FP8_E4M3 = 0, 1
 KDA_DEVERR_SLOT, KDA_DEVERR_ACCEPTED, KDA_DEVERR_TIMEOUT, KDA_DEVERR_DECAY = 0x1, 0x2, 0x4, 0x8
 KDA_DEVERR_TOKENS, KDA_DEVERR_SEQLEN = 0x10, 0x20
 KDA_DEVERR_PAGE, KDA_DEVERR_NOPAGES = 0x40, 0x80
-KDA_T_BF16, KDA_T_F16, KDA_T_E4M3 = 0, 1, 2
+KDA_T_BF16, KDA_T_F16, KDA_T_E4M3, KDA_T_E2M1 = 0, 1, 2, 4
 DK = DV = RANK = 128
 CONV_K = 4
 PREFILL_CHUNK = 64
@@ -78,6 +78,8 @@ def _load() -> ctypes.CDLL:
         "kda_kv_fork": [P, P, P, I32, P, SZ, P],
         "kda_kv_compact": [P, P, P, SZ, P],
         "kda_kv_append": [P, I32, P, I32, I32, P, P, P, P, P, P, P],
+        "kda_rope": [P, I32, P, I32, I32, P, P, P, P, P, P, P],
+        "kda_kv_append_rope": [P, I32, P, P, I32, I32, P, P, P, P, P, P, P, P, P, P],
         "kda_attn_decode": [P, I32, P, P, I32, I32, P, P, P, P, P, SZ, P],
         "kda_attn_prefill": [P, I32, P, P, I32, P, I32, I32, P, P, P, P, SZ, P],
         "kda_kv_get_error": [P, P, P],
@@ -111,7 +113,7 @@ EXPORTS = ("kda_decode", "kda_verify", "kda_commit", "kda_decode_resume", "kda_v
            "kda_get_error", "kda_status_string", "kda_last_error", "kda_abi_version",
            "kda_prefill_noalloc", "kda_prefill_noalloc_max_bytes",
            "kda_kv_workspace_size", "kda_kv_extend", "kda_kv_truncate", "kda_kv_fork", "kda_kv_compact",
-           "kda_kv_append", "kda_attn_workspace_size", "kda_attn_decode", "kda_attn_prefill",
+           "kda_kv_append", "kda_rope", "kda_kv_append_rope", "kda_attn_workspace_size", "kda_attn_decode", "kda_attn_prefill",
            "kda_kv_get_error")
 
 

@@ -17,9 +17,11 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from .kda import (KDA_DEVERR_TIMEOUT, KDA_ERR_DEVICE, KDA_OK, KDA_T_BF16, KDA_T_E4M3, KDA_T_F16, _call, _lib, _need, _ptr, _raise, _stream)
+from .kda import (KDA_DEVERR_TIMEOUT, KDA_ERR_DEVICE, KDA_OK, KDA_T_BF16, KDA_T_E2M1, KDA_T_E4M3, KDA_T_F16, _call, _lib, _need, _ptr, _raise, _stream)
 
-_TYPES = {torch.bfloat16: KDA_T_BF16, torch.float16: KDA_T_F16, torch.float8_e4m3fn: KDA_T_E4M3}
+# of a cache; uint8 is the storage of a 4-bit one
+_TYPES = {torch.bfloat16: KDA_T_BF16, torch.float16: KDA_T_F16, torch.float8_e4m3fn: KDA_T_E4M3, torch.uint8: KDA_T_E2M1}
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
 class _Cache(ctypes.Structure):
@@ -45,13 +47,16 @@ class _Desc(ctypes.Structure):
 
 @dataclass
 class KdaKvCache:
-    """Caller-owned paged cache (see kda_kv_cache in include/kda.h)."""
-    k: torch.Tensor            # bf16, f16 or float8_e4m3fn [layers, pages, Hkv, page size, D]
+    """Caller-owned paged cache (see kda_kv_cache in include/kda.h).
+
+    A 4-bit cache (E2M1 codes with an E4M3 scale for each 16 elements) is held as uint8 [layers, pages, Hkv, page size,
+    D / 2 + D / 16]: the bytes of a page's head are those of all its codes and then those of all its block scales."""
+    k: torch.Tensor            # bf16, f16 or float8_e4m3fn [layers, pages, Hkv, page size, D], or uint8 as above
     v: torch.Tensor            # like k
     page_table: torch.Tensor   # int32 [rows, max_pages], -1 where there is no page
     seq_lens: torch.Tensor     # int32 [rows]
     page_refs: torch.Tensor    # int32 [pages]: table entries that name each page
-    k_scale: Optional[torch.Tensor] = None   # f32 [layers, Hkv] with float8_e4m3fn
+    k_scale: Optional[torch.Tensor] = None   # f32 [layers, Hkv] with float8_e4m3fn and uint8
     v_scale: Optional[torch.Tensor] = None
     err_word: Optional[torch.Tensor] = None  # int32 [1], zeroed; made here if not given
 
@@ -63,9 +68,9 @@ class KdaKvCache:
     @staticmethod
     def zeros(layers: int, num_pages: int, Hkv: int, rows: int, max_pages: int, page_size: int = 64,
               head_dim: int = 128, dtype=torch.bfloat16, device="cuda", k_scale=None, v_scale=None) -> "KdaKvCache":
-        """An empty cache; with float8_e4m3fn the scales are ones unless given."""
-        shape = (layers, num_pages, Hkv, page_size, head_dim)
-        if dtype == torch.float8_e4m3fn:
+        """An empty cache; with float8_e4m3fn and uint8 (4 bits) the scales are ones unless given."""
+        shape = (layers, num_pages, Hkv, page_size, head_dim // 2 + head_dim // 16 if dtype == torch.uint8 else head_dim)
+        if dtype in _CODES:
             k_scale = torch.ones(layers, Hkv, device=device) if k_scale is None else k_scale
             v_scale = torch.ones(layers, Hkv, device=device) if v_scale is None else v_scale
         raw = torch.uint8 if dtype == torch.float8_e4m3fn else dtype
@@ -85,7 +90,7 @@ class KdaKvCache:
 
     @property
     def head_dim(self) -> int:
-        return self.k.shape[4]
+        return self.k.shape[4] * 16 // 9 if self.k.dtype == torch.uint8 else self.k.shape[4]
 
     @property
     def num_pages(self) -> int:
@@ -112,11 +117,15 @@ class KdaKvCache:
         if cached is not None and cached[2] == ptrs:
             return cached
         if self.k.dtype not in _TYPES:
-            raise TypeError(f"k: dtype {self.k.dtype}, expected bfloat16, float16 or float8_e4m3fn")
+            raise TypeError(f"k: dtype {self.k.dtype}, expected bfloat16, float16, float8_e4m3fn or uint8 (4 bits)")
         if self.k.dim() != 5:
             raise ValueError(f"k: shape {tuple(self.k.shape)}, expected [layers, pages, Hkv, page size, D]")
         dev = self.k.device
         layers, pages, Hkv, ps, D = self.k.shape
+        if self.k.dtype == torch.uint8:
+            if D % 9:
+                raise ValueError(f"k: shape {tuple(self.k.shape)}, a 4-bit cache has D / 2 + D / 16 bytes for each token")
+            D = self.head_dim
         _need(self.k, "k", self.k.dtype, self.k.shape, dev)
         _need(self.v, "v", self.k.dtype, self.k.shape, dev)
         if self.page_table.dim() != 2:
@@ -126,15 +135,15 @@ class KdaKvCache:
         _need(self.seq_lens, "seq_lens", torch.int32, (rows,), dev)
         _need(self.page_refs, "page_refs", torch.int32, (pages,), dev)
         _need(self.err_word, "err_word", torch.int32, (1,), dev)
-        fp8 = self.k.dtype == torch.float8_e4m3fn
-        if fp8:
+        codes = self.k.dtype in _CODES
+        if codes:
             for name, t in (("k_scale", self.k_scale), ("v_scale", self.v_scale)):
                 if t is None:
-                    raise ValueError(f"{name} is required with a float8_e4m3fn cache")
+                    raise ValueError(f"{name} is required with a {'4-bit' if self.k.dtype == torch.uint8 else 'float8_e4m3fn'} cache")
                 _need(t, name, torch.float32, (layers, Hkv), dev)
         st = _Cache(_ptr(self.k), _ptr(self.v), _TYPES[self.k.dtype], layers, pages, Hkv, ps, D, rows, width,
                     _ptr(self.page_table), _ptr(self.seq_lens), _ptr(self.page_refs),
-                    _ptr(self.k_scale) if fp8 else None, _ptr(self.v_scale) if fp8 else None, _ptr(self.err_word))
+                    _ptr(self.k_scale) if codes else None, _ptr(self.v_scale) if codes else None, _ptr(self.err_word))
         d.pop("_plans", None)
         d["_c_struct"] = cached = (st, ctypes.byref(st), ptrs, dev)
         self._make_workspaces()
@@ -148,7 +157,7 @@ class KdaKvCache:
         if self.k.dim() != 5 or self.page_table.dim() != 2:
             return
         capturing = _capturing(dev)
-        st = _Cache(num_pages=self.k.shape[1], head_dim=self.k.shape[4], rows=self.page_table.shape[0])
+        st = _Cache(num_pages=self.k.shape[1], head_dim=self.head_dim, rows=self.page_table.shape[0])
         made = False
         for kind, size in (("_kv_ws", _lib.kda_kv_workspace_size), ("_attn_ws", _lib.kda_attn_workspace_size)):
             n, old = max(256, int(size(ctypes.byref(st)))), d.get(kind)
@@ -259,7 +268,7 @@ def _tokens(t: torch.Tensor, name: str, packed: bool, heads: Optional[int], cach
     D, dev = cache.head_dim, cache.device
     if t.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 or float16")
-    if cache.k.dtype != torch.float8_e4m3fn and cache.k.dtype != t.dtype:
+    if cache.k.dtype not in _CODES and cache.k.dtype != t.dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, the cache holds {cache.k.dtype}")
     n = t.shape
     if len(n) != (3 if packed else 4) or n[-1] != D or (heads is not None and n[-2] != heads):
