@@ -78,6 +78,13 @@ __device__ __forceinline__ void e2m1x8_half8(uint32_t w, uint32_t *h)
         "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
+// The low four bits of x's bytes, the high four of y's (one instruction; as two masks it takes two).
+__device__ __forceinline__ uint32_t low_nibbles_of(uint32_t x, uint32_t y)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xca;" : "=r"(r) : "r"(0x0f0f0f0fu), "r"(x), "r"(y));
+    return r;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
 {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));

@@ -28,8 +28,7 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kStep = 16;                 // keys of one warp step
-constexpr int kTileKeys = kWarps * kStep; // keys of one tile: 16 for each warp
+constexpr int kStep = 16;                 // keys of a product
 constexpr int kMaxCtas = 1024;            // bound of the grid, sizes the workspace
 constexpr int kUnitRows = 32;
 // A unit counts for this many tiles more than it has: starting one (queries, page ids, the first keys,
@@ -56,6 +55,20 @@ __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ... from zero
+template <typename T>
+__device__ __forceinline__ void mma16816_zero(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    if constexpr (T::is_half)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Transposes an 8x8 matrix of 16-bit elements held one row per quad.
@@ -103,14 +116,22 @@ struct Cfg {
     static constexpr int RB = KV == kKv16 ? D * 2 : KV == kKvE4M3 ? D : D / 2;   // bytes of a key (its codes)
     static constexpr int SB = KV == kKvE2M1 ? D / 16 : 0; // ... and of its block scales
     static constexpr int CH = RB / 16;                    // 16-byte chunks of a key
-    static constexpr int STAGE = 2 * kStep * (RB + SB);   // keys, values, then both's block scales
+    // Keys of a warp's step.  Two groups of 16 with 4 bits: their page ids, addresses, bounds and maximum took as many
+    // instructions as a third of their arithmetic.  256 sequences of 1 to 4096 tokens, 8 heads: 139 us with 16 keys, 120 with
+    // 32 (and addresses kept from step to step); in long runs 5.8 TB/s.
+    static constexpr int KEYS = KV == kKvE2M1 ? 2 * kStep : kStep, TILE = kWarps * KEYS;   // ... and of a tile: a step of each warp
+    static constexpr int STAGE = 2 * KEYS * (RB + SB);    // keys, values, then both's block scales
+    static constexpr int V_AT = KEYS * RB, KS_AT = 2 * V_AT, VS_AT = KS_AT + KEYS * SB;
     // CTAs of an SM: as many as the accumulators (D NB / 4 registers) leave room for.  A warp's step is a
     // chain of latencies (scores, exponentials, product), which other warps cover: two CTAs everywhere
     // against this, 64 x 4096 tokens, 8 heads, E4M3: 153 us, 129 us; bfloat16 (HBM bound) 171 us both.
     static constexpr int OCC = D * NB >= 512 ? 2 : (RB == 256 || D * NB >= 256) ? 3 : 4;
     static constexpr bool Q_SMEM = NB > 1;                // queries in shared memory instead of registers
     static constexpr int Q_BYTES = Q_SMEM ? NB * 8 * D * 2 : 0;
-    static constexpr int NS_FIT = (220 * 1024 / OCC - 2048 - Q_BYTES) / (kWarps * STAGE);
+    // Sequences whose (row, length, tokens) are kept on chip.  E2M1: three stages and four CTAs take all of the 228 KB but 2 KB a CTA.
+    static constexpr int SEQS = KV == kKvE2M1 ? 224 : 256;
+    static constexpr int NS_FIT = KV == kKvE2M1 ? (228 * 1024 / OCC - 1024 - 8 * SEQS - 128 - Q_BYTES) / (kWarps * STAGE)
+                                                : (220 * 1024 / OCC - 2048 - Q_BYTES) / (kWarps * STAGE);
     static constexpr int NS = NS_FIT > 6 ? 6 : NS_FIT;    // stages of a warp's ring
     static constexpr int RING = kWarps * NS * STAGE;
     // the pieces of a unit are merged in the ring's place
@@ -178,12 +199,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
     // type of both products: E4M3 codes are exact halves, and so are E2M1 codes times their E4M3 scale (two bits by
     // four, 2^-10 to 2688)
     using P = std::conditional_t<CODES, Half, Q>;
-    constexpr int kSeqs = 256;                    // sequences whose (row, length, tokens) are kept on chip
+    constexpr int kSeqs = C::SEQS;
     constexpr int MT = D / 16;                    // accumulator blocks (16 head dims)
     constexpr int ROWS = 8 * NB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long sh_prefix, sh_warp[kWarps];
-    __shared__ int sh_b, sh_last, sh_units[kWarps], sh_most[kWarps], sh_seq[3][kSeqs];
+    __shared__ int sh_b, sh_last, sh_units[kWarps], sh_most[kWarps], sh_seq[2][kSeqs];   // row and tokens, length
     const PagedCache &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, cc = lane & 3;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
@@ -200,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
     auto tiles_of = [&](const SeqInfo &s, int &kt, int &mt) -> long long {   // kt tiles in each of Hkv * mt units
         kt = mt = 0;
         if (!s.ok || s.n == 0) return 0;
-        const KeyRange<kTileKeys> r(s.len - s.n, s.len - 1, s.len, W, S);
+        const KeyRange<C::TILE> r(s.len - s.n, s.len - 1, s.len, W, S);
         kt = max(1, r.count);
         mt = (s.n * p.G + ROWS - 1) / ROWS;
         return (long long)(place ? place : kt + kUnitCost) * mt * c.Hkv;
@@ -210,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
     int kt, mt, units = 0, most = 0;   // (units: 2^20 at most)
     for (int b = b_lo; b < b_hi; b++) {
         const SeqInfo s = load_seq(b, blockIdx.x == 0);
-        if (b < kSeqs) sh_seq[0][b] = s.row, sh_seq[1][b] = s.len, sh_seq[2][b] = s.ok ? s.n : 0;
+        if (b < kSeqs) sh_seq[0][b] = (s.row & (kMaxRows - 1)) | (s.ok ? s.n : 0) * kMaxRows, sh_seq[1][b] = s.len;
         mine += tiles_of(s, kt, mt);
         units = min(units + mt * c.Hkv, 1 << 20);
         if (mt) most = max(most, kt + kUnitCost);
@@ -218,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
     auto seq_of = [&](int b) {   // after the barrier below
         if (b >= kSeqs) return load_seq(b, false);
         SeqInfo s;
-        s.row = sh_seq[0][b], s.len = sh_seq[1][b], s.n = sh_seq[2][b], s.ok = true;
+        s.row = sh_seq[0][b] & (kMaxRows - 1), s.len = sh_seq[1][b], s.n = sh_seq[0][b] / kMaxRows, s.ok = true;
         return s;
     };
     long long before = mine;
@@ -290,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
     float *mg_m = mg + kWarps * ROWS * D, *mg_l = mg_m + kWarps * ROWS;
 
     int pages_of = -1, first_now = -1, first_next = -1;   // whose pages of tiles 0 to 63 this lane holds
+    [[maybe_unused]] int first_now2 = -1, first_next2 = -1;
     long long at = begin;
     while (at < end) {
         while (at >= prefix + seq_tiles) {   // next sequence with work (there is one: at < total)
@@ -304,14 +326,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
         const int ta = (int)(max(at, u0) - u0), tb = (int)min((long long)kt, end - u0);
         const int n_rows = min(ROWS, seq.n * p.G - mb * ROWS);
         const int p0 = seq.len - seq.n;
-        const KeyRange<kTileKeys> kr(p0, seq.len - 1, seq.len, W, S);
+        const KeyRange<C::TILE> kr(p0, seq.len - 1, seq.len, W, S);
         const int lo_all = (int)max(0ll, (long long)seq.len - W);         // every token sees [lo_all, p0]
         const uint32_t page_bytes = (uint32_t)c.page_bytes();   // under 2^27
         const uint8_t *k_head = c.k + ((size_t)p.layer * c.pages * c.Hkv + h) * ((size_t)c.ps * (C::RB + C::SB)), *k_base = k_head + lane * 16;
         const ptrdiff_t v_minus_k = c.v - c.k;
-        // E2M1: lanes 0 to 15 copy the block scales of a step's keys, the others those of its values
-        const uint8_t *sc_base = k_head + (lane < kStep ? 0 : v_minus_k) + (size_t)c.ps * C::RB + (lane % kStep) * C::SB;
-        const uint32_t dst_s = 2 * kStep * C::RB + lane * C::SB;
+        // E2M1: lanes copy 16 bytes of a step's block scales, the first half of them keys', the others values'; with pages of
+        // 16 tokens a step has two pages, whose halves of the scales are each other lanes'
+        constexpr int SC = 2 * C::KEYS * C::SB / 16;
+        const bool two_pages = KV == kKvE2M1 && c.ps < C::KEYS, second = two_pages && lane % max(1, SC / 2) >= SC / 4;
+        const uint8_t *sc_base = KV == kKvE2M1 ? k_head + (lane < SC / 2 ? 0 : v_minus_k) + (size_t)c.ps * C::RB + lane % max(1, SC / (two_pages ? 4 : 2)) * 16 : nullptr;
         // where a lane's pieces go: the swizzles of a step's rows differ from its first row's by constants
         const uint32_t dst_k = (lane / C::CH) * C::RB + (((lane % C::CH) ^ C::swz_k(lane / C::CH)) * 16);
         const uint32_t dst_v = KV == kKvE2M1 ? C::v_at(lane / C::CH, lane % C::CH)
@@ -379,33 +403,95 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
         for (int nb = 0; nb < NB; nb++) row_m[nb][0] = row_m[nb][1] = -INFINITY, row_l[nb][0] = row_l[nb][1] = 0.f;
 
         // page ids of this warp's next 32 steps, one per lane, and of the 32 after them
-        auto key_of = [&](int t) { return kr.tile(t) * kTileKeys + w * kStep; };
+        // (E2M1: `sub` is the step's second group of 16 keys; its page is another one where pages have 16 tokens)
+        auto key_of = [&](int t) { return kr.tile(t) * C::TILE + w * C::KEYS; };
         auto step_used = [&](int k0) { return k0 < kr.end && (k0 + kStep > kr.lo || k0 < S); };
-        auto load_pages = [&](int t0) {
+        [[maybe_unused]] auto step4_used = [&](int k0) { return k0 < kr.end && (k0 + C::KEYS > kr.lo || k0 < S); };
+        auto load_pages = [&](int t0, int sub) {
             const int t = t0 + lane;
             if (t >= kt) return -1;
-            const int k0 = key_of(t);
-            return step_used(k0) ? __ldg(c.table + (size_t)seq.row * c.width + (k0 >> c.ps_log2)) : -1;
+            const int k0 = key_of(t) + sub * kStep;
+            const bool used = KV != kKvE2M1 || two_pages ? step_used(k0) : sub == 0 && step4_used(k0);
+            return used ? __ldg(c.table + (size_t)seq.row * c.width + (k0 >> c.ps_log2)) : -1;
         };
         // a sequence's next unit (another head, the same pages) begins with those of its last one
         int pages_at = ta, pages_now, pages_next;
-        if (ta == 0 && pages_of == b) pages_now = first_now, pages_next = first_next;
-        else {
-            pages_now = load_pages(ta);
-            pages_next = load_pages(ta + 32);
-            if (ta == 0) pages_of = b, first_now = pages_now, first_next = pages_next;
+        [[maybe_unused]] int pages_now2, pages_next2;
+        if (ta == 0 && pages_of == b) {
+            pages_now = first_now, pages_next = first_next;
+            if constexpr (KV == kKvE2M1) pages_now2 = first_now2, pages_next2 = first_next2;
+        } else {
+            pages_now = load_pages(ta, 0);
+            pages_next = load_pages(ta + 32, 0);
+            if constexpr (KV == kKvE2M1) pages_now2 = load_pages(ta, 1), pages_next2 = load_pages(ta + 32, 1);
+            if (ta == 0) {
+                pages_of = b, first_now = pages_now, first_next = pages_next;
+                if constexpr (KV == kKvE2M1) first_now2 = pages_now2, first_next2 = pages_next2;
+            }
         }
 
-        uint32_t bad = 0;   // bit s: the step in stage s has no page
+        uint32_t bad = 0;   // bit s: the step in stage s has no page; E2M1: two bits, for its groups
+        [[maybe_unused]] auto issue4 = [&](int k0, int page, int page2, int stage) {
+            const uint32_t to = ring + stage * C::STAGE, in = k0 & (c.ps - 1);
+            constexpr int HALF = kStep * C::RB;
+            if (k0 + C::KEYS <= kr.end && (k0 >= kr.lo || k0 + C::KEYS <= S) && (unsigned)page < (unsigned)c.pages && (unsigned)page2 < (unsigned)c.pages) {
+                // some token sees every key, and all have a page
+                if (bad) bad &= ~(3u << 2 * stage);
+                const uint8_t *s1 = k_base + (size_t)(uint32_t)page * page_bytes + in * C::RB, *s2 = s1 + v_minus_k;
+                const uint32_t dk = to + lane * 16, dv = to + C::V_AT + dst_v;
+#pragma unroll
+                for (int i = 0; i < HALF; i += 512) cp16(dk + i, s1 + i), cp16(dv + i, s2 + i);
+                if (two_pages) {
+                    const uint8_t *s3 = k_base + (size_t)(uint32_t)page2 * page_bytes, *s4 = s3 + v_minus_k;
+#pragma unroll
+                    for (int i = 0; i < HALF; i += 512) cp16(dk + HALF + i, s3 + i), cp16(dv + HALF + i, s4 + i);
+                } else {
+#pragma unroll
+                    for (int i = HALF; i < 2 * HALF; i += 512) cp16(dk + i, s1 + i), cp16(dv + i, s2 + i);
+                }
+                if (SC == 32 || lane < SC) cp16(dk + C::KS_AT, sc_base + (size_t)(uint32_t)(second ? page2 : page) * page_bytes + in * C::SB);
+                return;
+            }
+            if (!step4_used(k0)) return;
+            for (int sub = 0; sub < 2; sub++) {   // zeros for the keys that no token sees, or that have no page
+                const int g0 = k0 + sub * kStep, pg = sub ? page2 : page;
+                // (a step's two groups are in one page where pages have more than 16 tokens, whichever of them is seen)
+                const bool used = step_used(g0), ok = used && (unsigned)pg < (unsigned)c.pages;
+                bad = used && !ok ? bad | (1u << (2 * stage + sub)) : bad & ~(1u << (2 * stage + sub));
+                if (used && !ok && lane == 0) atomicOr(c.err, KDA_DEVERR_PAGE);
+                const uint8_t *head = k_head + (ok ? (size_t)(uint32_t)pg * page_bytes : 0);
+                const int row0 = g0 & (c.ps - 1);
+                constexpr int PER = 32 / C::CH;
+#pragma unroll
+                for (int i = 0; i < kStep / PER; i++) {
+                    const int r = i * PER + lane / C::CH, j = g0 + r;
+                    const bool read = ok && j < kr.end && (j >= kr.lo || j < S);
+                    const uint8_t *src = head + (row0 + r) * C::RB + lane % C::CH * 16;
+                    const uint32_t dst = to + sub * kStep * C::RB;
+                    cp16_or_zero(dst + lane * 16 + i * 512, src, read);
+                    cp16_or_zero(dst + C::V_AT + dst_v + i * 512, src + v_minus_k, read);
+                }
+                const int r = lane % kStep, j = g0 + r;   // block scales: half the lanes keys', the others values'
+                cp_scales<C::SB>(to + (lane < kStep ? C::KS_AT : C::VS_AT) + (sub * kStep + r) * C::SB,
+                                 head + (lane < kStep ? 0 : v_minus_k) + (size_t)c.ps * C::RB + (row0 + r) * C::SB,
+                                 ok && j < kr.end && (j >= kr.lo || j < S));
+            }
+        };
         auto issue = [&](int t, int stage) {
             if (t < tb) {
                 if (t - pages_at >= 32) {
                     pages_at += 32;
                     pages_now = pages_next;
-                    pages_next = load_pages(pages_at + 32);
+                    pages_next = load_pages(pages_at + 32, 0);
+                    if constexpr (KV == kKvE2M1) pages_now2 = pages_next2, pages_next2 = load_pages(pages_at + 32, 1);
                 }
                 const int k0 = key_of(t);
                 const int page = __shfl_sync(~0u, pages_now, t - pages_at);
+                if constexpr (KV == kKvE2M1) {
+                    issue4(k0, page, two_pages ? __shfl_sync(~0u, pages_now2, t - pages_at) : page, stage);
+                    cp_async_commit();
+                    return;
+                }
                 if (step_used(k0)) {
                     const bool ok = (unsigned)page < (unsigned)c.pages;
                     bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
@@ -422,7 +508,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
                                 cp16(dk + i * 512, sk + i * 512);
                                 cp16(dv + i * 512 + (dst_v ^ (C::swz_v(i * PER) * 16)), sv + i * 512);
                             }
-                            if constexpr (KV == kKvE2M1) cp_scales<C::SB>(ring + stage * C::STAGE + dst_s, sc_base + (size_t)(uint32_t)page * page_bytes + (k0 & (c.ps - 1)) * C::SB, true);
                         } else {   // zeros for the keys that no token sees
 #pragma unroll
                             for (int i = 0; i < kStep / PER; i++) {
@@ -431,16 +516,142 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
                                 cp16_or_zero(dk + i * 512, sk + i * 512, read);
                                 cp16_or_zero(dv + i * 512 + (dst_v ^ (C::swz_v(i * PER) * 16)), sv + i * 512, read);
                             }
-                            if constexpr (KV == kKvE2M1) {
-                                const int j = k0 + lane % kStep;
-                                cp_scales<C::SB>(ring + stage * C::STAGE + dst_s, sc_base + (size_t)(uint32_t)page * page_bytes + (k0 & (c.ps - 1)) * C::SB,
-                                                 j < kr.end && (j >= kr.lo || j < S));
-                            }
                         }
                     }
                 }
             }
             cp_async_commit();
+        };
+
+        // A step of 32 4-bit keys: the scores of both groups, one look at the maximum, both groups' values.
+        float row_b[NB][2] = {};   // row_m, but 0 while a row has seen no key
+        // Where this lane's values and their block scales are in a stage: row 2 cc; row 2 cc + 1 is in the neighbouring chunks, D / 2
+        // bytes away (stages begin at multiples of 128 bytes).
+        const uint32_t vo = KV != kKvE2M1 ? 0 : C::V_AT + C::v_at(2 * cc, D == 128 ? g >> 1 : g >> 2) + (D == 128 ? 8 * (g & 1) : 4 * (g & 3));
+        const uint32_t vso = C::VS_AT + 2 * cc * C::SB + (D == 128 ? g : g >> 1);
+        static_assert(KV != kKvE2M1 || C::STAGE % 128 == 0, "");
+        [[maybe_unused]] auto step4 = [&](int k0, int stage) {
+            const uint32_t at = ring + stage * C::STAGE, at_k = at + lane * (D / 8), at_ks = at + lane * (D / 64), at_v = at + vo, at_v1 = at_v ^ (D / 2), at_vs = at + vso;
+            float s[2][NB][4];
+#pragma unroll
+            for (int sub = 0; sub < 2; sub++) {
+                // a quarter of the key for each lane, one or two blocks of 16 elements
+                constexpr int NW = D / 32;
+                uint32_t xs[NW], ys[NW], sx[2], sy[2];
+                const uint32_t kb = at_k + sub * kStep * C::RB, ks = at_ks + C::KS_AT + sub * kStep * C::SB;
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(kb), y = lds128(kb + 8 * C::RB);
+                    xs[0] = x.x, xs[1] = x.y, xs[2] = x.z, xs[3] = x.w;
+                    ys[0] = y.x, ys[1] = y.y, ys[2] = y.z, ys[3] = y.w;
+                    const uint32_t a = e4m3x2_half2(lds_u16(ks)), b = e4m3x2_half2(lds_u16(ks + 8 * C::SB));
+                    sx[0] = __byte_perm(a, a, 0x1010), sx[1] = __byte_perm(a, a, 0x3232);
+                    sy[0] = __byte_perm(b, b, 0x1010), sy[1] = __byte_perm(b, b, 0x3232);
+                } else {
+                    const uint2 x = lds64(kb), y = lds64(kb + 8 * C::RB);
+                    xs[0] = x.x, xs[1] = x.y, ys[0] = y.x, ys[1] = y.y;
+                    sx[0] = e4m3x2_half2(lds_u8(ks) * 0x101u), sy[0] = e4m3x2_half2(lds_u8(ks + 8 * C::SB) * 0x101u);
+                }
+#pragma unroll
+                for (int u = 0; u < NW; u++) {
+                    uint32_t x[4], y[4];
+                    e2m1x8_half8(xs[u], x);
+                    e2m1x8_half8(ys[u], y);
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint32_t a[4] = {hmul2(x[2 * i], sx[u / 2]), hmul2(y[2 * i], sy[u / 2]), hmul2(x[2 * i + 1], sx[u / 2]), hmul2(y[2 * i + 1], sy[u / 2])};
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++) {
+                            uint2 q;
+                            if constexpr (C::Q_SMEM) q = lds64(q_at + (nb * (D / 16) + 2 * u + i) * 256);
+                            else q = make_uint2(qf[2 * u + i][0], qf[2 * u + i][1]);
+                            if (u == 0 && i == 0) mma16816_zero<P>(s[sub][nb], a, q.x, q.y);
+                            else mma16816<P>(s[sub][nb], a, q.x, q.y);
+                        }
+                    }
+                }
+            }
+            // s[sub][nb]: keys k0 + 16 sub + g (+ 8), rows nb * 8 + 2 cc (+ 1); in units of log2
+            if (!(k0 + C::KEYS - 1 <= p0 && (k0 >= lo_all || k0 + C::KEYS <= S) && bad == 0)) {
+#pragma unroll
+                for (int sub = 0; sub < 2; sub++)
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            if ((bad >> (2 * stage + sub) & 1) || !key_visible(k0 + sub * kStep + g + 8 * (i >> 1), row_pos[nb][i & 1], W, S)) s[sub][nb][i] = -INFINITY;
+            }
+            bool grown = false;
+            float top[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    top[nb][i] = fmaxf(fmaxf(s[0][nb][i], s[0][nb][i + 2]), fmaxf(s[1][nb][i], s[1][nb][i + 2])) * sc[nb][i];
+                    grown |= top[nb][i] > row_m[nb][i] + (P::kShift + P::kGrow);
+                }
+            if (__any_sync(~0u, grown)) {
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        float mx = top[nb][i];
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                        const float m_new = fmaxf(row_m[nb][i], mx - P::kShift);
+                        const float alpha = m_new == -INFINITY ? 1.f : ex2(row_m[nb][i] - m_new);
+                        row_m[nb][i] = m_new;
+                        row_b[nb][i] = m_new == -INFINITY ? 0.f : m_new;
+                        row_l[nb][i] *= alpha;
+#pragma unroll
+                        for (int m = 0; m < MT; m++) acc[m][nb][i] *= alpha, acc[m][nb][2 + i] *= alpha;
+                    }
+            }
+#pragma unroll
+            for (int sub = 0; sub < 2; sub++) {
+                uint32_t pf[NB][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++) {
+                    float(&x)[4] = s[sub][nb];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) x[i] = ex2(fmaf(x[i], sc[nb][i & 1], -row_b[nb][i & 1]));
+                    row_l[nb][0] += x[0] + x[2];
+                    row_l[nb][1] += x[1] + x[3];
+                    // P is rounded to halves for the product (down to 2^-25 of the largest); l sums it unrounded
+                    pf[nb][0] = transpose8x8(P::pack(x[0], x[1]));
+                    pf[nb][1] = transpose8x8(P::pack(x[2], x[3]));
+                }
+                constexpr int NW = D / 64;   // words of 8 codes per thread and key, all of one block
+                uint32_t v[4][NW], sv[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {   // keys 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9
+                    const uint32_t from = ((i & 1) ? at_v1 : at_v) + (sub * kStep + 8 * (i >> 1)) * C::RB;
+                    if constexpr (NW == 2) {
+                        const uint2 x = lds64(from);
+                        v[i][0] = x.x, v[i][1] = x.y;
+                    } else {
+                        v[i][0] = lds32(from);
+                    }
+                    sv[i] = lds_u8(at_vs + (sub * kStep + (i & 1) + 8 * (i >> 1)) * C::SB);
+                }
+                const uint32_t s01 = e4m3x2_half2(__byte_perm(sv[0], sv[1], 0x0040)), s23 = e4m3x2_half2(__byte_perm(sv[2], sv[3], 0x0040));
+#pragma unroll
+                for (int u = 0; u < NW; u++) {
+                    // the same element's codes of two keys in one byte before the conversion
+                    uint32_t e[2][2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint32_t x = v[2 * i][u], y = v[2 * i + 1][u];
+                        e2m1x8_half8(low_nibbles_of(x, y << 4), e[0][i]);
+                        e2m1x8_half8(low_nibbles_of(x >> 4, y), e[1][i]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const uint32_t a[4] = {hmul2(e[0][0][j], s01), hmul2(e[1][0][j], s01), hmul2(e[0][1][j], s23), hmul2(e[1][1][j], s23)};
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++) mma16816<P>(acc[4 * u + j][nb], a, pf[nb][0], pf[nb][1]);
+                    }
+                }
+            }
         };
 
         int st_in = 0, st_out = 0;
@@ -453,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
             __syncwarp();
             const int k0 = key_of(t), stage = st_out;
             st_out = st_out + 1 == C::NS ? 0 : st_out + 1;
-            if (step_used(k0) && !(bad >> stage & 1)) {
+            if constexpr (KV == kKvE2M1) {
+                if (step4_used(k0)) step4(k0, stage);
+            } else if (step_used(k0) && !(bad >> stage & 1)) {
                 const uint32_t kb = ring + stage * C::STAGE, vb = kb + kStep * C::RB;
                 float s[NB][4], s2[NB][4];   // one row block: two chains of products, added at the end
 #pragma unroll
@@ -469,54 +682,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
                         mma16816<P>(NB == 1 && (kb_ & 1) ? s2[nb] : s[nb], a, q.x, q.y);
                     }
                 };
-                if constexpr (KV == kKvE2M1) {
-                    // a quarter of the key for each lane, one or two blocks of 16 elements
-                    constexpr int NW = D / 32;
-                    uint32_t xs[NW], ys[NW], sx[2], sy[2];
-                    const uint32_t ks = kb + 2 * kStep * C::RB;
-                    if constexpr (D == 128) {
-                        const uint4 x = lds128(kb + g * C::RB + cc * 16), y = lds128(kb + (g + 8) * C::RB + cc * 16);
-                        xs[0] = x.x, xs[1] = x.y, xs[2] = x.z, xs[3] = x.w;
-                        ys[0] = y.x, ys[1] = y.y, ys[2] = y.z, ys[3] = y.w;
-                        const uint32_t a = e4m3x2_half2(lds_u16(ks + g * C::SB + 2 * cc)), b = e4m3x2_half2(lds_u16(ks + (g + 8) * C::SB + 2 * cc));
-                        sx[0] = __byte_perm(a, a, 0x1010), sx[1] = __byte_perm(a, a, 0x3232);
-                        sy[0] = __byte_perm(b, b, 0x1010), sy[1] = __byte_perm(b, b, 0x3232);
-                    } else {
-                        const uint2 x = lds64(kb + g * C::RB + cc * 8), y = lds64(kb + (g + 8) * C::RB + cc * 8);
-                        xs[0] = x.x, xs[1] = x.y, ys[0] = y.x, ys[1] = y.y;
-                        sx[0] = e4m3x2_half2(lds_u8(ks + g * C::SB + cc) * 0x101u), sy[0] = e4m3x2_half2(lds_u8(ks + (g + 8) * C::SB + cc) * 0x101u);
-                    }
 #pragma unroll
-                    for (int u = 0; u < NW; u++) {
-                        uint32_t x[4], y[4];
-                        e2m1x8_half8(xs[u], x);
-                        e2m1x8_half8(ys[u], y);
+                for (int j = 0; j < C::CH / 4; j++) {
+                    const uint4 x = lds128(kb + g * C::RB + (((cc + 4 * j) ^ C::swz_k(g)) * 16));
+                    const uint4 y = lds128(kb + (g + 8) * C::RB + (((cc + 4 * j) ^ C::swz_k(g + 8)) * 16));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                    if constexpr (CODES) {
 #pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const uint32_t a[4] = {hmul2(x[2 * i], sx[u / 2]), hmul2(y[2 * i], sy[u / 2]), hmul2(x[2 * i + 1], sx[u / 2]), hmul2(y[2 * i + 1], sy[u / 2])};
-                            qk(2 * u + i, a);
+                        for (int u = 0; u < 4; u++) {
+                            uint32_t a[4];
+                            e4m3x4_half4(xs[u], a[0], a[2]);
+                            e4m3x4_half4(ys[u], a[1], a[3]);
+                            qk(4 * j + u, a);
                         }
-                    }
-                } else {
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < C::CH / 4; j++) {
-                        const uint4 x = lds128(kb + g * C::RB + (((cc + 4 * j) ^ C::swz_k(g)) * 16));
-                        const uint4 y = lds128(kb + (g + 8) * C::RB + (((cc + 4 * j) ^ C::swz_k(g + 8)) * 16));
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-                        if constexpr (CODES) {
-#pragma unroll
-                            for (int u = 0; u < 4; u++) {
-                                uint32_t a[4];
-                                e4m3x4_half4(xs[u], a[0], a[2]);
-                                e4m3x4_half4(ys[u], a[1], a[3]);
-                                qk(4 * j + u, a);
-                            }
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 2; u++) {
-                                const uint32_t a[4] = {xs[2 * u], ys[2 * u], xs[2 * u + 1], ys[2 * u + 1]};
-                                qk(2 * j + u, a);
-                            }
+                        for (int u = 0; u < 2; u++) {
+                            const uint32_t a[4] = {xs[2 * u], ys[2 * u], xs[2 * u + 1], ys[2 * u + 1]};
+                            qk(2 * j + u, a);
                         }
                     }
                 }
@@ -584,39 +767,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
                         }
 #pragma unroll
                         for (int i = 0; i < 4; i++) pv(4 * hh + i, v[0][i], v[1][i], v[2][i], v[3][i]);
-                    }
-                } else if constexpr (KV == kKvE2M1) {
-                    constexpr int NW = D / 64;   // words of 8 codes per thread and key, all of one block
-                    uint32_t v[4][NW], sv[4];
-                    const uint32_t vs = vb + kStep * (C::RB + C::SB);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        if constexpr (NW == 2) {
-                            const uint2 x = lds64(vb + C::v_at(kk[i], g >> 1) + 8 * (g & 1));
-                            v[i][0] = x.x, v[i][1] = x.y;
-                            sv[i] = lds_u8(vs + kk[i] * C::SB + g);
-                        } else {
-                            v[i][0] = lds32(vb + C::v_at(kk[i], g >> 2) + 4 * (g & 3));
-                            sv[i] = lds_u8(vs + kk[i] * C::SB + (g >> 1));
-                        }
-                    }
-                    const uint32_t s01 = e4m3x2_half2(sv[0] | sv[1] << 8), s23 = e4m3x2_half2(sv[2] | sv[3] << 8);
-#pragma unroll
-                    for (int u = 0; u < NW; u++) {
-                        // the same element's codes of two keys in one byte before the conversion
-                        uint32_t e[2][2][4];
-#pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const uint32_t x = v[2 * i][u], y = v[2 * i + 1][u];
-                            e2m1x8_half8((x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u), e[0][i]);
-                            e2m1x8_half8((x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), e[1][i]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const uint32_t a[4] = {hmul2(e[0][0][j], s01), hmul2(e[1][0][j], s01), hmul2(e[0][1][j], s23), hmul2(e[1][1][j], s23)};
-#pragma unroll
-                            for (int nb = 0; nb < NB; nb++) mma16816<P>(acc[4 * u + j][nb], a, pf[nb][0], pf[nb][1]);
-                        }
                     }
                 } else {
                     constexpr int NW = D / 32;   // words of 4 codes per thread and key
@@ -779,7 +929,7 @@ cudaError_t launch_as(const AttnParams &p, cudaStream_t stream)
 {
     static KernelSetup setup;
     constexpr int smem = Cfg<D, KV, NB>::SMEM;
-    static_assert(Cfg<D, KV, NB>::NS >= 2 && Cfg<D, KV, NB>::NS <= 32, "a ring of two stages at least");
+    static_assert(Cfg<D, KV, NB>::NS >= 2 && Cfg<D, KV, NB>::NS <= 16, "a ring of two stages at least");
     int resident = 0;
     const cudaError_t e = setup.get(kda_attn_decode_kernel<D, Q, KV, NB>, kThreads, smem, 0, &resident);
     if (e != cudaSuccess) return e;
