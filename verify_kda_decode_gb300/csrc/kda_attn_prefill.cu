@@ -81,6 +81,7 @@ struct Smem {
     uint8_t kv[kSlots][kKeys * D * 2];
     uint8_t raw[KV != kKv16 ? kRaw : 1][KV != kKv16 ? kKeys * KeyBytes<D, KV>::RB : 16];
     uint8_t raw_scale[KV == kKvE2M1 ? kRaw : 1][KV == kKvE2M1 ? kKeys * KeyBytes<D, KV>::SB : 16];
+    uint64_t raw_full[kRaw], raw_empty[kRaw], q_raw;   // E2M1: raw items, and queries, of warp 14
     uint64_t q_full[2], q_empty, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], u_full[kUnits], u_empty[kUnits], join, drain;
     unsigned gone[kGone];                   // by the tile's number: groups of 8 keys that are seen but have no page
     Unit unit[kUnits];
@@ -358,8 +359,9 @@ __device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, 
 template <int D, typename Q, int KV>
 __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int W, int S, uint32_t &item, uint32_t &units)
 {
+    using SM = Smem<D, KV>;
     const AttnParams &p = args.p;
-    constexpr uint32_t kSlots = Smem<D, KV>::kSlots;
+    constexpr uint32_t kSlots = SM::kSlots;
     const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
     const PagedCache &c = p.c;
     const int tid = threadIdx.x - kSoftmax, w = tid >> 5, lane = tid & 31, r8 = lane & 7, q4 = lane >> 3;
@@ -376,12 +378,13 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
         if (i >= n || lane >= kKeys / 8 || k0 >= kr.end || !(k0 + 8 > kr.lo || k0 < S)) return 0;
         return __ldg(c.table + (size_t)u.row * c.width + (k0 >> c.ps_log2));
     };
-    int pages = pages_of(0), pages_next = pages_of(1);
+    int pages = 0, pages_next = 0;
+    if constexpr (KV != kKvE2M1) pages = pages_of(0), pages_next = pages_of(1);
     // Which groups are seen but have no page, for the softmax: written ahead of this thread's arrival for the tile's keys,
     // which their products wait for.  The word of the tile four before has been read by then: an item written now (or
     // sent three items ahead, E4M3) has waited for the keys of the tile three before it at least, whose products
     // are only issued when the softmax has handed over the tile before them.
-    auto tell_gone = [&](uint32_t ring) {
+    [[maybe_unused]] auto tell_gone = [&](uint32_t ring) {
         const unsigned gone = __ballot_sync(~0u, (unsigned)pages >= (unsigned)c.pages);
         if (tid == 0 && !(ring & 1)) sm.gone[(ring >> 1) % kGone] = gone;
         return gone;
@@ -448,15 +451,15 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
         tc::fence_smem_to_async();
         mbar_arrive(&sm.q_full[units & 1]);
     };
-    // source of key r of group gi of tile i, this many bytes a key from `at` on in its page; null where nothing is read
-    auto source = [&](const uint8_t *base, int i, int gi, int pg, int r, size_t at, int bytes) -> const uint8_t * {
-        const int k0 = kr.tile(u.ta + i) * kKeys + gi * 8, j = k0 + r;
+    // source of this lane's key of group gi of tile i; null where nothing is read
+    [[maybe_unused]] auto source = [&](const uint8_t *base, int i, int gi, int pg) -> const uint8_t * {
+        const int k0 = kr.tile(u.ta + i) * kKeys + gi * 8, j = k0 + r8;
         if (!(j < kr.end && (j >= kr.lo || j < S))) return nullptr;
         if ((unsigned)pg >= (unsigned)c.pages) {
             atomicOr(c.err, KDA_DEVERR_PAGE);
             return nullptr;
         }
-        return base + (((size_t)p.layer * c.pages + pg) * c.Hkv + u.h) * head_bytes + at + (size_t)(j & (c.ps - 1)) * bytes;
+        return base + (((size_t)p.layer * c.pages + pg) * c.Hkv + u.h) * head_bytes + (size_t)(j & (c.ps - 1)) * RB;
     };
     if constexpr (!CODES) {
         for (int it = 0; it < 2 * n; it++) {
@@ -484,7 +487,7 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
 #pragma unroll
                 for (int a = 0; a < GR; a++) {
                     const int gi = w + 4 * a;
-                    const uint8_t *src = source(base, i, gi, __shfl_sync(~0u, pages, gi), r8, 0, RB);
+                    const uint8_t *src = source(base, i, gi, __shfl_sync(~0u, pages, gi));
 #pragma unroll
                     for (int x = 0; x < PASS; x++)
                         cp_async16(sm.kv[slot] + chunk_at(gi * 8 + r8, x * 4 + q4), src ? src + (x * 4 + q4) * 16 : c.k, src ? 16 : 0);
@@ -500,41 +503,80 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
                 pages_next = pages_of(i + 2);
             }
         }
+    } else if constexpr (KV == kKvE2M1) {
+        // Warp 14 fetches the codes (fetch_unit); these warps only convert them, 32 keys each.
+        constexpr int ROWS = 32 / CPR;   // a pass: chunk cp of ROWS keys
+        const int row = lane % ROWS, cp = lane / ROWS;
+        for (int it = 0; it < 2 * n; it++) {
+            const uint32_t ring = item + it;
+            const int slot = ring % kSlots, from = ring % SM::kRaw;
+            if (!wait_warp(sm, &sm.raw_full[from], (ring / SM::kRaw) & 1, c.err)) return false;
+            if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
+            const uint8_t *src = sm.raw[from] + (w * 32 + row) * RB + cp * 16, *sc = sm.raw_scale[from] + (w * 32 + row) * SB + 2 * cp;
+#pragma unroll
+            for (int a = 0; a < CPR; a++) {   // 32 codes, two blocks: exact in halves
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + a * ROWS * RB);
+                const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t s2 = e4m3x2_half2(*reinterpret_cast<const uint16_t *>(sc + a * ROWS * SB));
+                const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+#pragma unroll
+                for (int y = 0; y < 4; y++) {
+                    uint32_t e[4];
+                    e2m1x8_half8(ws[y], e);
+                    *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at(w * 32 + a * ROWS + row, cp * 4 + y)) =
+                        make_uint4(hmul2(e[0], s[y >> 1]), hmul2(e[1], s[y >> 1]), hmul2(e[2], s[y >> 1]), hmul2(e[3], s[y >> 1]));
+                }
+            }
+            tc::fence_smem_to_async();
+            mbar_arrive(&sm.full[slot]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.raw_empty[from]);
+            if (it == 0) {   // the first keys were converted while the last unit's queries were still in use
+                if (!Q::is_half && args.q_map) {
+                    // bfloat16 queries came as they are (fetch_unit): brought to [1, 2) and to halves in place, a row a thread
+                    if (!wait_warp(sm, &sm.q_raw, units & 1, c.err)) return false;
+                    for (int hf = 0; hf < u.halves; hf++) {
+                        uint8_t *q = sm.q[hf];
+                        uint32_t mag = 0;
+#pragma unroll
+                        for (int g = 0; g < D / 8; g++) mag = max_magnitude(mag, *reinterpret_cast<const uint4 *>(q + chunk_at(tid, g)));
+                        float down, up;
+                        query_scale(mag, down, up);
+#pragma unroll
+                        for (int g = 0; g < D / 8; g++) {
+                            uint4 *x = reinterpret_cast<uint4 *>(q + chunk_at(tid, g));
+                            *x = scaled_halves(*x, down);
+                        }
+                        sm.q_scale[units & 1][hf * kHalf + tid] = up;
+                    }
+                    tc::fence_smem_to_async();
+                    mbar_arrive(&sm.q_full[units & 1]);
+                } else {
+                    if (!load_queries()) return false;
+                    queries_done();
+                }
+            }
+        }
     } else {
         if (!load_queries()) return false;
         queries_done();
         // Codes come to shared memory three items ahead (each thread's own pieces, so that only its own copies are
         // waited for) and are converted (exactly) to halves on their way into the ring.  With one item ahead,
         // in registers, a tile pair took 3.0 us; like this 2.5 us (16-bit caches: 1.54).
-        // E2M1: passes of KPP of the warp's 32 keys, a lane takes chunk cp of its kp-th; and one key's block scales, which
-        // the multiplications by them (exact, too) read from any lane's key of the warp.
-        constexpr int kRaw = Smem<D, KV>::kRaw, KPP = 32 / CPR;
-        [[maybe_unused]] const int kp = lane % KPP, cp = lane / KPP;
+        constexpr int kRaw = Smem<D, KV>::kRaw;
         int sent = 0;   // items whose copies are under way
         auto send = [&]() {
             if (sent < 2 * n) {
                 tell_gone(item + sent);
                 const uint8_t *base = sent & 1 ? c.v : c.k;
                 uint8_t *dst = sm.raw[sent % kRaw] + tid * 16;
-                if constexpr (KV == kKvE2M1) {
 #pragma unroll
-                    for (int a = 0; a < CPR; a++) {
-                        const int key = a * KPP + kp, gi = w + 4 * (key >> 3);
-                        const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi), key & 7, 0, RB);
-                        cp_async16(dst + a * (kLoaders * 16), src ? src + cp * 16 : c.k, src ? 16 : 0);
-                    }
-                    const int gi = w + 4 * (lane >> 3);
-                    const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi), r8, (size_t)c.ps * RB, SB);
-                    cp_async_small<SB>(sm.raw_scale[sent % kRaw] + tid * SB, src ? src : c.k, src ? SB : 0);
-                } else {
+                for (int a = 0; a < GR; a++) {
+                    const int gi = w + 4 * a;
+                    const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi));
 #pragma unroll
-                    for (int a = 0; a < GR; a++) {
-                        const int gi = w + 4 * a;
-                        const uint8_t *src = source(base, sent >> 1, gi, __shfl_sync(~0u, pages, gi), r8, 0, RB);
-#pragma unroll
-                        for (int x = 0; x < PASS; x++)
-                            cp_async16(dst + (a * PASS + x) * (kLoaders * 16), src ? src + (x * 4 + q4) * 16 : c.k, src ? 16 : 0);
-                    }
+                    for (int x = 0; x < PASS; x++)
+                        cp_async16(dst + (a * PASS + x) * (kLoaders * 16), src ? src + (x * 4 + q4) * 16 : c.k, src ? 16 : 0);
                 }
                 if (sent & 1) {
                     pages = pages_next;
@@ -549,44 +591,22 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
             const uint32_t ring = item + it;
             const int slot = ring % kSlots;
             cp_async_wait<kRaw - 1>();
-            if constexpr (KV == kKvE2M1) __syncwarp();   // the block scales of the warp's keys, which its other lanes fetched
             if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
             const uint4 *src = reinterpret_cast<const uint4 *>(sm.raw[it % kRaw]) + tid;
-            if constexpr (KV == kKvE2M1) {
-                const uint8_t *scales = sm.raw_scale[it % kRaw] + w * 32 * SB;
 #pragma unroll
-                for (int a = 0; a < CPR; a++) {   // 32 codes, two blocks
-                    const int key = a * KPP + kp;
-                    const uint4 v = src[a * kLoaders];
+            for (int a = 0; a < GR; a++)
+#pragma unroll
+                for (int x = 0; x < PASS; x++) {
+                    const uint4 v = src[(a * PASS + x) * kLoaders];
                     const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
-                    const uint32_t s2 = e4m3x2_half2(*reinterpret_cast<const uint16_t *>(scales + key * SB + 2 * cp));
-                    const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
-                    const int row = (w + 4 * (key >> 3)) * 8 + (key & 7);
+                    uint32_t e[8];
 #pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        uint32_t e[4];
-                        e2m1x8_half8(ws[y], e);
-                        *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at(row, cp * 4 + y)) =
-                            make_uint4(hmul2(e[0], s[y >> 1]), hmul2(e[1], s[y >> 1]), hmul2(e[2], s[y >> 1]), hmul2(e[3], s[y >> 1]));
-                    }
+                    for (int s = 0; s < 4; s++) e4m3x4_half4(ws[s], e[2 * s], e[2 * s + 1]);
+#pragma unroll
+                    for (int s = 0; s < 2; s++)
+                        *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at((w + 4 * a) * 8 + r8, (x * 4 + q4) * 2 + s)) =
+                            make_uint4(e[4 * s], e[4 * s + 1], e[4 * s + 2], e[4 * s + 3]);
                 }
-                __syncwarp();   // read by all lanes before the next fetch
-            } else {
-#pragma unroll
-                for (int a = 0; a < GR; a++)
-#pragma unroll
-                    for (int x = 0; x < PASS; x++) {
-                        const uint4 v = src[(a * PASS + x) * kLoaders];
-                        const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t e[8];
-#pragma unroll
-                        for (int s = 0; s < 4; s++) e4m3x4_half4(ws[s], e[2 * s], e[2 * s + 1]);
-#pragma unroll
-                        for (int s = 0; s < 2; s++)
-                            *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at((w + 4 * a) * 8 + r8, (x * 4 + q4) * 2 + s)) =
-                                make_uint4(e[4 * s], e[4 * s + 1], e[4 * s + 2], e[4 * s + 3]);
-                    }
-            }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.full[slot]);
             send();
@@ -596,6 +616,118 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
     item += 2 * n;
     units++;
     return true;
+}
+
+// ---- warp 14, 4-bit cache: a unit's codes and block scales as they are (raw items 2 i and 2 i + 1 of tile i), whole pages by bulk
+// copies, and its bfloat16 queries
+template <int D, typename Q>
+__device__ bool fetch_unit(Smem<D, kKvE2M1> &sm, const Args &args, const Unit &u, int W, int S, uint32_t &item, uint32_t &units, uint32_t &written)
+{
+    using SM = Smem<D, kKvE2M1>;
+    constexpr int RB = KeyBytes<D, kKvE2M1>::RB, SB = KeyBytes<D, kKvE2M1>::SB, CPR = RB / 16, ROWS = 32 / CPR;
+    const AttnParams &p = args.p;
+    const PagedCache &c = p.c;
+    const int lane = threadIdx.x & 31, n = u.tb - u.ta;
+    const KeyRange<kKeys> kr(u.p_first, u.p_last, u.len, W, S);
+    const uint32_t page_bytes = (uint32_t)c.page_bytes();   // under 2^27
+    const size_t head_bytes = (size_t)c.ps * (RB + SB);
+    const uint8_t *k_head = c.k + ((size_t)p.layer * c.pages * c.Hkv + u.h) * head_bytes;
+    const ptrdiff_t v_minus_k = c.v - c.k;
+    // page of key group `lane` (16 groups of a tile), 0 where none of its keys is seen (and no page is looked at)
+    auto pages_of = [&](int i) {
+        const int k0 = kr.tile(u.ta + i) * kKeys + lane * 8;
+        if (i >= n || lane >= kKeys / 8 || k0 >= kr.end || !(k0 + 8 > kr.lo || k0 < S)) return 0;
+        return __ldg(c.table + (size_t)u.row * c.width + (k0 >> c.ps_log2));
+    };
+    int pages = pages_of(0), pages_next = pages_of(1);
+    for (int i = 0; i < n; i++) {
+        const int k0 = kr.tile(u.ta + i) * kKeys;
+        const unsigned gone = __ballot_sync(~0u, (unsigned)pages >= (unsigned)c.pages);
+        const bool whole = gone == 0 && k0 + kKeys <= kr.end && (k0 >= kr.lo || k0 + kKeys <= S);
+        // lane x: page x of the tile
+        const int tile_pages = kKeys >> c.ps_log2 ? kKeys >> c.ps_log2 : 1, page = __shfl_sync(~0u, pages, (lane << (c.ps_log2 - 3)) & 31);
+        const uint8_t *head = k_head + (size_t)(uint32_t)page * page_bytes;
+        for (int kv = 0; kv < 2; kv++) {
+            const uint32_t ring = item + 2 * i + kv;
+            const int to = ring % SM::kRaw;
+            uint64_t *bar = &sm.raw_full[to];
+            const ptrdiff_t add = kv ? v_minus_k : 0;
+            if (ring >= SM::kRaw && !wait_warp(sm, &sm.raw_empty[to], (ring / SM::kRaw - 1) & 1, c.err)) return false;
+            // (told ahead of the tile's keys, see tell_gone: its raw item has waited for the conversion of the one kRaw items before)
+            if (kv == 0 && lane == 0) sm.gone[(ring >> 1) % kGone] = gone;
+            if (whole) {
+                if (written >> to & 1) {   // before a bulk copy overwrites what these lanes' copies wrote
+                    tc::fence_smem_to_async();
+                    written &= ~(1u << to);
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_expect_tx(bar, kKeys * (RB + SB));
+                else mbar_arrive(bar);
+                __syncwarp();
+                if (lane < tile_pages) {
+                    const uint32_t codes = (uint32_t)(RB << c.ps_log2), scales = (uint32_t)(SB << c.ps_log2);
+                    bulk_load(sm.raw[to] + lane * codes, head + add, codes, bar);
+                    bulk_load(sm.raw_scale[to] + lane * scales, head + add + codes, scales, bar);
+                }
+            } else {   // zeros for the keys that no token sees, or that have no page
+                auto key = [&](int r) -> const uint8_t * {   // head of its page, null: zeros
+                    const int j = k0 + r, pg = __shfl_sync(~0u, pages, r >> 3);
+                    if (!(j < kr.end && (j >= kr.lo || j < S))) return nullptr;
+                    if ((unsigned)pg >= (unsigned)c.pages) {
+                        atomicOr(c.err, KDA_DEVERR_PAGE);
+                        return nullptr;
+                    }
+                    return k_head + (size_t)(uint32_t)pg * page_bytes + add;
+                };
+                for (int r = lane % ROWS; r < kKeys; r += ROWS) {
+                    const uint8_t *h = key(r);
+                    cp_async16(sm.raw[to] + r * RB + lane / ROWS * 16, h ? h + ((k0 + r) & (c.ps - 1)) * RB + lane / ROWS * 16 : c.k, h ? 16 : 0);
+                }
+                for (int r = lane; r < kKeys; r += 32) {
+                    const uint8_t *h = key(r);
+                    cp_async_small<SB>(sm.raw_scale[to] + r * SB, h ? h + (size_t)c.ps * RB + ((k0 + r) & (c.ps - 1)) * SB : c.k, h ? SB : 0);
+                }
+                written |= 1u << to;
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+            }
+            if constexpr (!Q::is_half)
+                if (i == 0 && kv == 0 && args.q_map) {   // rows past the unit's are other tokens' (or zeros), and what comes of them is not stored
+                    if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.q_raw, u.halves * (kHalf * D * 2));
+                    __syncwarp();
+                    if (lane < u.halves * (D / 64)) {
+                        const int hf = lane / (D / 64), x = lane % (D / 64);
+                        tma_load_3d(smem_u32(sm.q[0]) + hf * (kHalf * D * 2) + x * kHalfBytes, &args.q, x * 64, u.h * p.G,
+                                    u.c0 + (u.r0 + hf * kHalf) / p.G, &sm.q_raw);
+                    }
+                }
+        }
+        pages = pages_next;
+        pages_next = pages_of(i + 2);
+    }
+    item += 2 * n;
+    units++;
+    return true;
+}
+
+template <int D, typename Q, int KV>
+__device__ void fetch_role(Smem<D, KV> &sm, const Args &args, int W, int S)
+{
+    if constexpr (KV == kKvE2M1) {
+        uint32_t item = 0, units = 0, written = 0;
+        for (int k = 0; const Unit *at = unit_of(sm, k, args.p.c.err); k++) {
+            const Unit u = *at;
+            unit_done(sm, k);
+            if (u.tb > u.ta && !fetch_unit<D, Q>(sm, args, u, W, S, item, units, written)) break;
+        }
+        cp_async_wait<0>();
+        // where a wait gave up, copies may still be landing: let them
+        if (sm.stop) {
+            for (int i = 0; i < Smem<D, KV>::kRaw; i++)
+                for (uint32_t parity = 0; parity < 2; parity++) mbar_wait_bounded(&sm.raw_full[i], parity, kLimitNs / 16);
+            for (uint32_t parity = 0; parity < 2; parity++) mbar_wait_bounded(&sm.q_raw, parity, kLimitNs / 16);
+        }
+    }
 }
 
 template <int D, typename Q, int KV>
@@ -991,6 +1123,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.join, kSoftmax / 32);
         mbar_init(&sm.drain, 1);
+        mbar_init(&sm.q_raw, 1);
+        for (int i = 0; i < Smem<D, KV>::kRaw; i++) {
+            mbar_init(&sm.raw_full[i], 32);
+            mbar_init(&sm.raw_empty[i], kLoaders / 32);
+        }
         for (int i = 0; i < (int)Smem<D, KV>::kSlots; i++) {
             mbar_init(&sm.full[i], kLoaders);
             mbar_init(&sm.empty[i], 1);
@@ -1002,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
         }
         for (int i = 0; i < kUnits; i++) {
             mbar_init(&sm.u_full[i], 1);
-            mbar_init(&sm.u_empty[i], 13);   // the warps of the other roles
+            mbar_init(&sm.u_empty[i], KV == kKvE2M1 ? 14 : 13);   // the warps of the other roles
         }
         sm.stop = 0;
         fence_mbar_init();
@@ -1055,6 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
         regs_dec<kRegsMma>();
         if (warp == 12) mma_role<D, std::conditional_t<KV != kKv16, Half, Q>>(sm, __reduce_max_sync(~0u, tmem), p.c.err);
         else if (warp == 13) unit_role(sm, p, W, S);
+        else if (KV == kKvE2M1 && warp == 14) fetch_role<D, Q, KV>(sm, args, W, S);
         __syncwarp();
         regs_inc<kRegs>();
     }
