@@ -354,6 +354,15 @@ __device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, 
     return (size_t)(u.c0 + t) * p.Hq + u.h * p.G + (u.r0 + x - t * p.G);
 }
 
+// Whether bfloat16 queries come as they are (by warp 14, 4-bit cache) and are brought to halves in place by the softmax's threads.
+template <typename Q, int KV>
+__device__ __forceinline__ bool queries_in_place(const Args &args) { return KV == kKvE2M1 && !Q::is_half && args.q_map; }
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // ---- warps 8-11: a unit's queries, then keys and values of tile i as ring items 2 i and 2 i + 1
 // (`item`: ring items so far, `units`: units so far)
 template <int D, typename Q, int KV>
@@ -506,13 +515,17 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
     } else if constexpr (KV == kKvE2M1) {
         // Warp 14 fetches the codes (fetch_unit); these warps only convert them, 32 keys each.
         constexpr int ROWS = 32 / CPR;   // a pass: chunk cp of ROWS keys
-        const int row = lane % ROWS, cp = lane / ROWS;
+        const int row = lane % ROWS, cp = lane / ROWS, at_codes = (w * 32 + row) * RB + cp * 16, at_scales = (w * 32 + row) * SB + 2 * cp;
+        int at_tile[4];   // (the rows of later passes are whole groups of 8 further: the same places in their swizzle)
+#pragma unroll
+        for (int y = 0; y < 4; y++) at_tile[y] = chunk_at(w * 32 + row, cp * 4 + y);
         for (int it = 0; it < 2 * n; it++) {
             const uint32_t ring = item + it;
             const int slot = ring % kSlots, from = ring % SM::kRaw;
             if (!wait_warp(sm, &sm.raw_full[from], (ring / SM::kRaw) & 1, c.err)) return false;
             if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
-            const uint8_t *src = sm.raw[from] + (w * 32 + row) * RB + cp * 16, *sc = sm.raw_scale[from] + (w * 32 + row) * SB + 2 * cp;
+            const uint8_t *src = sm.raw[from] + at_codes, *sc = sm.raw_scale[from] + at_scales;
+            const uint32_t dst = smem_u32(sm.kv[slot]);
 #pragma unroll
             for (int a = 0; a < CPR; a++) {   // 32 codes, two blocks: exact in halves
                 const uint4 v = *reinterpret_cast<const uint4 *>(src + a * ROWS * RB);
@@ -523,38 +536,17 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
                 for (int y = 0; y < 4; y++) {
                     uint32_t e[4];
                     e2m1x8_half8(ws[y], e);
-                    *reinterpret_cast<uint4 *>(sm.kv[slot] + chunk_at(w * 32 + a * ROWS + row, cp * 4 + y)) =
-                        make_uint4(hmul2(e[0], s[y >> 1]), hmul2(e[1], s[y >> 1]), hmul2(e[2], s[y >> 1]), hmul2(e[3], s[y >> 1]));
+                    sts128(dst + at_tile[y] + a * ROWS * 128, hmul2(e[0], s[y >> 1]), hmul2(e[1], s[y >> 1]), hmul2(e[2], s[y >> 1]), hmul2(e[3], s[y >> 1]));
                 }
             }
             tc::fence_smem_to_async();
             mbar_arrive(&sm.full[slot]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.raw_empty[from]);
-            if (it == 0) {   // the first keys were converted while the last unit's queries were still in use
-                if (!Q::is_half && args.q_map) {
-                    // bfloat16 queries came as they are (fetch_unit): brought to [1, 2) and to halves in place, a row a thread
-                    if (!wait_warp(sm, &sm.q_raw, units & 1, c.err)) return false;
-                    for (int hf = 0; hf < u.halves; hf++) {
-                        uint8_t *q = sm.q[hf];
-                        uint32_t mag = 0;
-#pragma unroll
-                        for (int g = 0; g < D / 8; g++) mag = max_magnitude(mag, *reinterpret_cast<const uint4 *>(q + chunk_at(tid, g)));
-                        float down, up;
-                        query_scale(mag, down, up);
-#pragma unroll
-                        for (int g = 0; g < D / 8; g++) {
-                            uint4 *x = reinterpret_cast<uint4 *>(q + chunk_at(tid, g));
-                            *x = scaled_halves(*x, down);
-                        }
-                        sm.q_scale[units & 1][hf * kHalf + tid] = up;
-                    }
-                    tc::fence_smem_to_async();
-                    mbar_arrive(&sm.q_full[units & 1]);
-                } else {
-                    if (!load_queries()) return false;
-                    queries_done();
-                }
+            // the first keys were converted while the last unit's queries were still in use (softmax_role converts queries that come by TMA)
+            if (it == 0 && !queries_in_place<Q, KV>(args)) {
+                if (!load_queries()) return false;
+                queries_done();
             }
         }
     } else {
@@ -691,7 +683,7 @@ __device__ bool fetch_unit(Smem<D, kKvE2M1> &sm, const Args &args, const Unit &u
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
             }
             if constexpr (!Q::is_half)
-                if (i == 0 && kv == 0 && args.q_map) {   // rows past the unit's are other tokens' (or zeros), and what comes of them is not stored
+                if (i == 0 && kv == 0 && queries_in_place<Q, kKvE2M1>(args)) {   // rows past the unit's are other tokens' (or zeros), and what comes of them is not stored
                     if (units > 0 && !wait_warp(sm, &sm.q_empty, (units - 1) & 1, c.err)) return false;
                     if (lane == 0) mbar_arrive_expect_tx(&sm.q_raw, u.halves * (kHalf * D * 2));
                     __syncwarp();
@@ -803,7 +795,7 @@ __device__ __noinline__ void join_row(const AttnParams &p, const Unit &u, const 
 // ---- warps 0-7: one thread per row (`tiles`, `units`: this half's key tiles and units so far; `all_units`:
 // those of either half, `all_tiles`: their key tiles)
 template <int D, typename Q, int KV>
-__device__ bool softmax_unit(Smem<D, KV> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, float *partial,
+__device__ bool softmax_unit(Smem<D, KV> &sm, const AttnParams &p, const Unit &u, uint32_t tmem, int W, int S, bool in_place, float q_up, float *partial,
                              uint32_t &tiles, uint32_t &units, uint32_t all_units, uint32_t all_tiles)
 {
     const PagedCache &c = p.c;
@@ -816,9 +808,12 @@ __device__ bool softmax_unit(Smem<D, KV> &sm, const AttnParams &p, const Unit &u
     using P = std::conditional_t<CODES, Half, Q>;                  // type of the products
     float row_scale = 1.f;
     if constexpr (CODES && !Q::is_half) {
-        // (the barrier of this parity cannot move on again before this half's last scores of the unit are read)
-        if (!wait_warp(sm, &sm.q_full[all_units & 1], (all_units >> 1) & 1, c.err)) return false;
-        row_scale = sm.q_scale[all_units & 1][x];
+        if (in_place) row_scale = q_up;
+        else {
+            // (the barrier of this parity cannot move on again before this half's last scores of the unit are read)
+            if (!wait_warp(sm, &sm.q_full[all_units & 1], (all_units >> 1) & 1, c.err)) return false;
+            row_scale = sm.q_scale[all_units & 1][x];
+        }
     }
     const float sc = score_scale(p.scale_log2 * (CODES ? c.k_scale[p.layer * c.Hkv + u.h] : 1.f) * row_scale);
     const int first = u.len - u.n;
@@ -926,6 +921,26 @@ __device__ bool softmax_unit(Smem<D, KV> &sm, const AttnParams &p, const Unit &u
     return true;
 }
 
+// Row r of a half's bfloat16 queries to halves in place, brought to [1, 2) by a power of two; returns what its scores have to be
+// multiplied with.
+template <int D>
+__device__ __forceinline__ float halve_row(uint8_t *q, int r)
+{
+    uint4 x[D / 8];
+    uint32_t mag = 0;
+#pragma unroll
+    for (int g = 0; g < D / 8; g++) {
+        x[g] = *reinterpret_cast<const uint4 *>(q + chunk_at(r, g));
+#pragma unroll
+        for (int i = 0; i < 4; i++) asm("max.u16x2 %0, %0, %1;" : "+r"(mag) : "r"((&x[g].x)[i] & 0x7fff7fffu));
+    }
+    float down, up;
+    query_scale(max(mag & 0xffffu, mag >> 16), down, up);
+#pragma unroll
+    for (int g = 0; g < D / 8; g++) *reinterpret_cast<uint4 *>(q + chunk_at(r, g)) = scaled_halves(x[g], down);
+    return up;
+}
+
 // Meeting point of the eight softmax warps, bounded like every wait.
 template <typename SM>
 __device__ __forceinline__ bool softmax_sync(SM &sm, uint32_t &joins, int *err)
@@ -936,8 +951,9 @@ __device__ __forceinline__ bool softmax_sync(SM &sm, uint32_t &joins, int *err)
 }
 
 template <int D, typename Q, int KV>
-__device__ void softmax_role(Smem<D, KV> &sm, const AttnParams &p, uint32_t tmem, int W, int S)
+__device__ void softmax_role(Smem<D, KV> &sm, const Args &args, uint32_t tmem, int W, int S)
 {
+    const AttnParams &p = args.p;
     const int tid = threadIdx.x, h = tid >> 7;
     int *count = reinterpret_cast<int *>(p.ws);
     SplitWs ws;
@@ -954,7 +970,16 @@ __device__ void softmax_role(Smem<D, KV> &sm, const AttnParams &p, uint32_t tmem
                 if (p.lse) p.lse[row] = -INFINITY;
             }
         } else {
-            if (h < u.halves && !softmax_unit<D, Q, KV>(sm, p, u, tmem, W, S, partial, tiles, units, all_units, all_tiles)) return;
+            float q_up = 1.f;
+            const bool in_place = queries_in_place<Q, KV>(args);
+            if (in_place) {   // this thread's row of queries, as halves
+                if (!wait_warp(sm, &sm.q_raw, all_units & 1, p.c.err)) return;
+                if (h < u.halves) q_up = halve_row<D>(sm.q[h], tid & 127);
+                tc::fence_smem_to_async();
+                __syncwarp();
+                if ((tid & 31) == 0) mbar_arrive(&sm.q_full[all_units & 1]);
+            }
+            if (h < u.halves && !softmax_unit<D, Q, KV>(sm, p, u, tmem, W, S, in_place, q_up, partial, tiles, units, all_units, all_tiles)) return;
             all_units++;
             all_tiles += u.tb - u.ta;
             if (partial) {
@@ -1119,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int W = p.window > 0 ? p.window : 0x7fffffff, S = p.window > 0 ? p.sinks : 0;
     if (tid == 0) {
-        for (int i = 0; i < 2; i++) mbar_init(&sm.q_full[i], kLoaders);   // by the unit's parity
+        for (int i = 0; i < 2; i++) mbar_init(&sm.q_full[i], queries_in_place<Q, KV>(args) ? kSoftmax / 32 : kLoaders);   // by the unit's parity
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.join, kSoftmax / 32);
         mbar_init(&sm.drain, 1);
@@ -1180,7 +1205,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
     const uint32_t tmem = sm.tmem;
     if (warp < 8) {
         regs_inc<kRegsSoftmax>();
-        softmax_role<D, Q, KV>(sm, p, tmem, W, S);
+        softmax_role<D, Q, KV>(sm, args, tmem, W, S);
         __syncwarp();
         regs_dec<kRegs>();   // back to what the common code was compiled for
     } else if (warp < 12) {
