@@ -129,6 +129,27 @@ def test_layouts_and_in_place(K, interleaved):
     assert (out[:, :, ::2] == 3).all()
 
 
+def test_calls_of_like_forms(K):
+    """Queries alone into a tensor that looks as keys would, then queries with such keys, and the other ways round."""
+    f = freqs_of(64)
+    rope = K.KdaRope.from_frequencies(f)
+    x = data((4, 9, 3, 64), BF, 8)
+    pos = torch.arange(9, dtype=torch.int32) * 77
+    q, k, a, b = x.cuda()
+    p = pos.cuda()
+    for _ in range(2):
+        assert K.kda_rope(rope, p, q, q_out=a) is a
+        check(a, x[0], pos, f, False, 1.0, BF)
+        gq, gk = K.kda_rope(rope, p, q, k)
+        check(gq, x[0], pos, f, False, 1.0, BF)
+        check(gk, x[1], pos, f, False, 1.0, BF)
+        gq, gk = K.kda_rope(rope, p, q, k, k_out=b)
+        assert gk is b and torch.equal(gq, a)
+        gq, gk = K.kda_rope(rope, p, q, k, q_out=a)
+        assert gq is a and torch.equal(gk, b)
+        check(K.kda_rope(rope, p, q), x[0], pos, f, False, 1.0, BF)
+
+
 def test_special_values(K):
     """A NaN or an infinity stays with its pair; the other pairs and the rest of the head are untouched by it."""
     f = freqs_of(32)

@@ -136,13 +136,11 @@ def _heads(t: torch.Tensor, name: str, D: int, dev) -> _Layout:
     return _Layout(_TYPES[t.dtype], 0 if len(n) == 3 or n[0] == 1 else st[0], 0 if n[-3] == 1 else st[-3], 0 if n[-2] == 1 else st[-2])
 
 
-def _copy_of(t, out, name: str):
-    """The tensor that receives t's turned copy."""
-    if out is None:
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _form(out, name: str):
+    """What the plan of a call into the caller's tensor goes by."""
     if not isinstance(out, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    return out
+    return out.dtype, out.device, out.shape, out.stride()
 
 
 def _turned(t, out, name: str, D: int, dev) -> _RopeLayout:
@@ -159,12 +157,21 @@ def kda_rope(rope: KdaRope, positions, q, k=None, q_out=None, k_out=None, stream
         raise TypeError("q and k must be torch.Tensors")
     dev = q.device
     _same_device(rope, dev)
-    _, ref, _ = rope._struct()
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    q_out = _copy_of(q, q_out, "q_out")
+    ref = rope._struct()[1]
+    # what this module makes itself is contiguous and of the inputs' form: such calls are found by the inputs alone
+    key = ("rope", dev, q.dtype, q.shape, q.stride())
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        key += ("q",) + _form(q_out, "q_out")
     if k is not None:
-        k_out = _copy_of(k, k_out, "k_out")
+        key += (k.dtype, k.device, k.shape, k.stride())
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        else:
+            key += ("k",) + _form(k_out, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
 
     def make():
         D = q.shape[-1] if q.dim() else 0
@@ -173,13 +180,10 @@ def kda_rope(rope: KdaRope, positions, q, k=None, q_out=None, k_out=None, stream
         if k is not None and (k.shape[:-2] != q.shape[:-2] or k.dtype != q.dtype):
             raise ValueError(f"q and k: {q.dtype} {tuple(q.shape)} and {k.dtype} {tuple(k.shape)} are not of the same tokens and type")
         B, T = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
-        return D, B, T, ctypes.byref(ql), None if kl is None else ctypes.byref(kl)
+        return q.shape[:-2], D, B, T, ctypes.byref(ql), None if kl is None else ctypes.byref(kl)
 
-    key = ("rope", dev, q.dtype, q.shape, q.stride(), q_out.dtype, q_out.device, q_out.shape, q_out.stride())
-    if k is not None:
-        key += (k.dtype, k.device, k.shape, k.stride(), k_out.dtype, k_out.device, k_out.shape, k_out.stride())
-    D, B, T, ql, kl = _plan(rope, key, make)
-    _need(positions, "positions", torch.int32, q.shape[:-2], dev)
+    tokens, D, B, T, ql, kl = _plan(rope, key, make)
+    _need(positions, "positions", torch.int32, tokens, dev)
     _call(dev, _lib.kda_rope, ref, D, positions.data_ptr(), B, T, ql, q.data_ptr(), q_out.data_ptr(), kl,
           None if k is None else k.data_ptr(), None if k is None else k_out.data_ptr(), _stream(stream, dev))
     return q_out if k is None else (q_out, k_out)
@@ -192,13 +196,18 @@ def kda_kv_append_rope(cache: KdaKvCache, layer: int, rows, rope: KdaRope, q, k,
     turned q (None without q); tokens that the append leaves out leave theirs as it was in q_out."""
     _, st, _, dev = cache._struct()
     _same_device(rope, dev)
-    _, ref, _ = rope._struct()
+    ref = rope._struct()[1]
     pr, B = _rows(rows, dev)
     for name, t in (("k", k), ("v", v)) + ((("q", q),) if q is not None else ()):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
+    key = ("append_rope", B, cu_seqlens is None, k.dtype, v.dtype, k.device, v.device, k.shape, v.shape, k.stride(), v.stride())
     if q is not None:
-        q_out = _copy_of(q, q_out, "q_out")
+        key += (q.dtype, q.device, q.shape, q.stride())
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            key += _form(q_out, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
 
@@ -228,9 +237,6 @@ def kda_kv_append_rope(cache: KdaKvCache, layer: int, rows, rope: KdaRope, q, k,
             T = k.shape[1]
         return T, None if ql is None else ctypes.byref(ql), ctypes.byref(kl), ctypes.byref(vl)
 
-    key = ("append_rope", B, cu_seqlens is None, k.dtype, v.dtype, k.device, v.device, k.shape, v.shape, k.stride(), v.stride())
-    if q is not None:
-        key += (q.dtype, q.device, q.shape, q.stride(), q_out.dtype, q_out.device, q_out.shape, q_out.stride())
     T, ql, kl, vl = _plan(cache, key, make)
     pc = None if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", B + 1, dev)
     pn = None if n_tokens is None else _ints(n_tokens, "n_tokens", B, dev)
