@@ -358,11 +358,6 @@ __device__ __forceinline__ size_t row_index(const AttnParams &p, const Unit &u, 
 template <typename Q, int KV>
 __device__ __forceinline__ bool queries_in_place(const Args &args) { return KV == kKvE2M1 && !Q::is_half && args.q_map; }
 
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
 // ---- warps 8-11: a unit's queries, then keys and values of tile i as ring items 2 i and 2 i + 1
 // (`item`: ring items so far, `units`: units so far)
 template <int D, typename Q, int KV>
@@ -525,7 +520,6 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
             if (!wait_warp(sm, &sm.raw_full[from], (ring / SM::kRaw) & 1, c.err)) return false;
             if (ring >= kSlots && !wait_warp(sm, &sm.empty[slot], (ring / kSlots - 1) & 1, c.err)) return false;
             const uint8_t *src = sm.raw[from] + at_codes, *sc = sm.raw_scale[from] + at_scales;
-            const uint32_t dst = smem_u32(sm.kv[slot]);
 #pragma unroll
             for (int a = 0; a < CPR; a++) {   // 32 codes, two blocks: exact in halves
                 const uint4 v = *reinterpret_cast<const uint4 *>(src + a * ROWS * RB);
@@ -536,7 +530,8 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
                 for (int y = 0; y < 4; y++) {
                     uint32_t e[4];
                     e2m1x8_half8(ws[y], e);
-                    sts128(dst + at_tile[y] + a * ROWS * 128, hmul2(e[0], s[y >> 1]), hmul2(e[1], s[y >> 1]), hmul2(e[2], s[y >> 1]), hmul2(e[3], s[y >> 1]));
+                    *reinterpret_cast<uint4 *>(sm.kv[slot] + at_tile[y] + a * ROWS * 128) =
+                        make_uint4(hmul2(e[0], s[y >> 1]), hmul2(e[1], s[y >> 1]), hmul2(e[2], s[y >> 1]), hmul2(e[3], s[y >> 1]));
                 }
             }
             tc::fence_smem_to_async();

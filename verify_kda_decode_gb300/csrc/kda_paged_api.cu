@@ -247,7 +247,7 @@ kda_status check_turned(const kda_kv_cache *cache, const kda_rope_layout *x, con
     CHECK(check_layout(cache, &x->src, name));
     CHECK(check_layout(cache, &x->dst, name));
     if (x->src.dtype != x->dst.dtype) return fail(KDA_ERR_INVALID_ARG, "%s and %s_out have different types", name, name);
-    if ((x->num_heads > 1 && x->dst.head_stride == 0) || (T > 1 && x->dst.token_stride == 0) || (B > 1 && x->dst.seq_stride == 0))
+    if (B > 0 && T > 0 && ((x->num_heads > 1 && x->dst.head_stride == 0) || (T > 1 && x->dst.token_stride == 0) || (B > 1 && x->dst.seq_stride == 0)))
         return fail(KDA_ERR_INVALID_ARG, "%s_out: its heads or tokens share memory", name);
     return KDA_OK;
 }

@@ -14,6 +14,9 @@ __device__ __forceinline__ float2 with_reciprocal(float scale)
     return make_float2(scale, a > 1e-18f && a < 1e18f ? __frcp_rn(scale) : NAN);
 }
 
+// (rarely called: kept out of the callers' code)
+static __device__ __noinline__ float quotient(float a, float b) { return __fdiv_rn(a, b); }
+
 // q = -g / scale.x, the IEEE quotients, of eight elements' negatives; `scale` from with_reciprocal.
 // Markstein's theorem gives that quotient from the correctly rounded reciprocal: q = f r, then q + (f - q scale) r, three
 // packed operations for two elements (a division each took 57 us for 33000 tokens to E4M3, bound by its instructions);
@@ -33,7 +36,7 @@ __device__ __forceinline__ void neg_quotients8(const float *g, float2 scale, flo
     }
     if (!(fabsf(t0 + t1) < 1e30f)) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) q[i] = __fdiv_rn(-g[i], scale.x);
+        for (int i = 0; i < 8; i++) q[i] = quotient(-g[i], scale.x);
     }
 }
 

@@ -18,7 +18,10 @@ namespace kda {
 namespace {
 
 constexpr int kWarpsCta = 8;
-constexpr int kAhead = 4;       // heads of a lane whose pieces are on their way at once
+// Heads of a lane whose pieces are on their way at once.  The rotation alone: two, each followed by the next one's load, in 24 warps
+// an SM (4 x 4096 tokens 55.6 us; three 57.2, four in 16 warps 59); the append: four at a time in 16 warps (32000 tokens to E4M3
+// 142 us; one by one 148, two in 24 warps 145).
+constexpr int kAhead = 2, kAheadAppend = 4;
 
 template <typename Q>
 __device__ __forceinline__ void unpack8(const uint4 &w, float *x)
@@ -53,62 +56,68 @@ struct Place {
     }
 };
 
-// Cosine and sine of the angles of a position, by the warp, in its shared memory.
-__device__ __forceinline__ void angles(const Turns &r, int pos, float2 *cs, int lane)
+// Cosines, then sines, of the angles of a position, by the warp, in its shared memory.
+__device__ __forceinline__ void angles(const Turns &r, int pos, float *cs, int lane)
 {
-    for (int f = lane; f < r.rot / 2; f += 32) {
+    const int n = r.rot / 2;
+    for (int f = lane; f < n; f += 32) {
         const long long turn = (long long)((unsigned long long)(long long)pos * __ldg(r.freq + f));
         float s, c;
         sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
-        cs[f] = make_float2(c * r.scale, s * r.scale);
+        cs[f] = c * r.scale;
+        cs[n + f] = s * r.scale;
     }
     __syncwarp();
 }
 
-// Eight pairs turned: (x0[i], x1[i]), or the neighbours in x0 and then in x1.
-__device__ __forceinline__ void turn8(float *x0, float *x1, const float2 *cs, bool adjacent)
+// A lane's eight cosines and sines.
+struct Angles { float c[8], s[8]; };
+__device__ __forceinline__ void load_angles(const Turns &r, const float *cs, int u, Angles &mine)
 {
-    if (adjacent) {
+    const float4 *c = reinterpret_cast<const float4 *>(cs + 8 * u), *s = reinterpret_cast<const float4 *>(cs + r.rot / 2 + 8 * u);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float a = x0[2 * i], b = x0[2 * i + 1], d = x1[2 * i], e = x1[2 * i + 1];
-            x0[2 * i] = fmaf(a, cs[i].x, -(b * cs[i].y));
-            x0[2 * i + 1] = fmaf(b, cs[i].x, a * cs[i].y);
-            x1[2 * i] = fmaf(d, cs[4 + i].x, -(e * cs[4 + i].y));
-            x1[2 * i + 1] = fmaf(e, cs[4 + i].x, d * cs[4 + i].y);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float a = x0[i], b = x1[i];
-            x0[i] = fmaf(a, cs[i].x, -(b * cs[i].y));
-            x1[i] = fmaf(b, cs[i].x, a * cs[i].y);
-        }
+    for (int i = 0; i < 2; i++) {
+        const float4 x = c[i], y = s[i];
+        mine.c[4 * i] = x.x, mine.c[4 * i + 1] = x.y, mine.c[4 * i + 2] = x.z, mine.c[4 * i + 3] = x.w;
+        mine.s[4 * i] = y.x, mine.s[4 * i + 1] = y.y, mine.s[4 * i + 2] = y.z, mine.s[4 * i + 3] = y.w;
     }
 }
 
-// A lane's cosines and sines.
-__device__ __forceinline__ void load_angles(const float2 *cs, int u, float2 *mine)
+// Two pairs (a0, b0), (a1, b1) turned, two elements an instruction.
+__device__ __forceinline__ void turn2(float &a0, float &a1, float &b0, float &b1, float c0, float c1, float s0, float s1)
 {
-    const float4 *at = reinterpret_cast<const float4 *>(cs + 8 * u);
+    float t0, t1, u0, u1;
+    tc::mul2(t0, t1, b0, b1, -s0, -s1);
+    tc::mul2(u0, u1, a0, a1, s0, s1);
+    tc::fma2(a0, a1, a0, a1, c0, c1, t0, t1);
+    tc::fma2(b0, b1, b0, b1, c0, c1, u0, u1);
+}
+// Eight pairs turned: (x0[i], x1[i]), or the neighbours in x0 and then in x1.
+__device__ __forceinline__ void turn8(float *x0, float *x1, const Angles &m, bool adjacent)
+{
+    if (adjacent) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float4 v = at[i];
-        mine[2 * i] = make_float2(v.x, v.y), mine[2 * i + 1] = make_float2(v.z, v.w);
+        for (int i = 0; i < 4; i += 2) {
+            turn2(x0[2 * i], x0[2 * i + 2], x0[2 * i + 1], x0[2 * i + 3], m.c[i], m.c[i + 1], m.s[i], m.s[i + 1]);
+            turn2(x1[2 * i], x1[2 * i + 2], x1[2 * i + 1], x1[2 * i + 3], m.c[4 + i], m.c[5 + i], m.s[4 + i], m.s[5 + i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) turn2(x0[i], x0[i + 1], x1[i], x1[i + 1], m.c[i], m.c[i + 1], m.s[i], m.s[i + 1]);
     }
 }
 
 template <typename Q>
-__global__ void __launch_bounds__(kWarpsCta * 32) kda_rope_kernel(const RopeParams p)
+__global__ void __launch_bounds__(kWarpsCta * 32, 3) kda_rope_kernel(const RopeParams p)
 {
-    extern __shared__ __align__(16) float2 all_angles[];
+    extern __shared__ __align__(16) float all_angles[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long id = (long long)blockIdx.x * kWarpsCta + warp;
     const int part = (int)(id % p.parts);
     const long long tok = id / p.parts;
     grid_dependency_wait();
     if (tok >= p.tokens) return;
-    float2 *cs = all_angles + warp * (p.r.rot / 2);
+    float *cs = all_angles + warp * p.r.rot;
     const int log2 = p.lanes_log2, u = lane & ((1 << log2) - 1), per = 32 >> log2;   // heads of a pass
     const Place at(p.r, u);
     const bool used = u < p.D / 16;
@@ -118,7 +127,7 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_rope_kernel(const RopePara
     const uint16_t *src[kAhead];
     uint16_t *dst[kAhead];
     uint4 a[kAhead], b[kAhead];
-    float2 mine[8];
+    Angles mine;
     auto load = [&](int pass, int j) {
         dst[j] = nullptr;
         if (pass >= n || !used) return;
@@ -130,28 +139,29 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_rope_kernel(const RopePara
         a[j] = __ldcs(reinterpret_cast<const uint4 *>(src[j]) + at.p0);
         b[j] = __ldcs(reinterpret_cast<const uint4 *>(src[j]) + at.p1);
     };
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) load(part + j * p.parts, j);
+    // while the first pieces are on their way
+    angles(p.r, pos, cs, lane);
+    if (at.turned) load_angles(p.r, cs, u, mine);
     for (int pass = part; pass < n; pass += kAhead * p.parts) {
 #pragma unroll
-        for (int j = 0; j < kAhead; j++) load(pass + j * p.parts, j);
-        if (pass == part) {   // while the first pieces are on their way
-            angles(p.r, pos, cs, lane);
-            if (at.turned) load_angles(cs, u, mine);
-        }
-#pragma unroll
         for (int j = 0; j < kAhead; j++) {
-            if (!dst[j]) continue;
-            if (at.turned) {
-                float x0[8], x1[8];
-                unpack8<Q>(a[j], x0);
-                unpack8<Q>(b[j], x1);
-                turn8(x0, x1, mine, p.r.adjacent);
-                a[j] = pack8<Q>(x0);
-                b[j] = pack8<Q>(x1);
-            } else if (src[j] == dst[j]) {
-                continue;   // in place: these stay
+            if (dst[j]) {
+                if (at.turned) {
+                    float x0[8], x1[8];
+                    unpack8<Q>(a[j], x0);
+                    unpack8<Q>(b[j], x1);
+                    turn8(x0, x1, mine, p.r.adjacent);
+                    a[j] = pack8<Q>(x0);
+                    b[j] = pack8<Q>(x1);
+                }
+                if (at.turned || src[j] != dst[j]) {   // (in place the rest stays)
+                    __stcs(reinterpret_cast<uint4 *>(dst[j]) + at.p0, a[j]);
+                    __stcs(reinterpret_cast<uint4 *>(dst[j]) + at.p1, b[j]);
+                }
             }
-            reinterpret_cast<uint4 *>(dst[j])[at.p0] = a[j];
-            reinterpret_cast<uint4 *>(dst[j])[at.p1] = b[j];
+            load(pass + (kAhead + j) * p.parts, j);   // its place is free again
         }
     }
 }
@@ -219,7 +229,7 @@ __device__ __forceinline__ void put_blocks(uint8_t *codes, uint8_t *scales, cons
 template <typename Q, int KV, bool TURN>
 __global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(const AppendTurnParams p)
 {
-    __shared__ __align__(16) float2 all_angles[kWarpsCta][TURN ? 64 : 2];
+    __shared__ __align__(16) float all_angles[kWarpsCta][TURN ? 128 : 4];
     const AppendParams &ap = p.a;
     const PagedCache &c = ap.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(cons
     const long long seq = ap.cu ? 0 : tok / ap.T, in_seq = tok - seq * ap.T;
     const long long row_k = (ap.cu ? 0 : seq * ap.kl.seq) + in_seq * ap.kl.token, row_v = (ap.cu ? 0 : seq * ap.vl.seq) + in_seq * ap.vl.token;
     const long long row_q = (ap.cu ? 0 : seq * p.q.sl.seq) + in_seq * p.q.sl.token, row_o = (ap.cu ? 0 : seq * p.q.dl.seq) + in_seq * p.q.dl.token;
-    uint4 a[kAhead], b[kAhead];
+    uint4 a[kAheadAppend], b[kAheadAppend];
     // pass: heads of the queries, then of the keys, then of the values
     auto head_of = [&](int pass) { return (pass < nq ? pass : pass < nq + nk ? pass - nq : pass - nq - nk) * per + mine_h; };
     auto load = [&](int pass, int j) {
@@ -249,68 +259,69 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(cons
     };
     // the first pieces are on their way while the token's place is found
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) load(part + j * p.parts, j);
+    for (int j = 0; j < kAheadAppend; j++) load(part + j * p.parts, j);
     int pos, page;
     if (!append_place(ap, tok, seq, in_seq, lane, lane == 0 && part == 0, pos, page)) return;
-    float2 mine[TURN ? 8 : 1];
+    [[maybe_unused]] Angles mine;
     if constexpr (TURN) {
         angles(p.r, pos, all_angles[warp], lane);
-        if (at.turned) load_angles(all_angles[warp], u, mine);
+        if (at.turned) load_angles(p.r, all_angles[warp], u, mine);
     }
     constexpr int SHIFT = KV == kKv16 ? 1 : 0;
     const int row_bytes = KV == kKvE2M1 ? c.D / 2 : c.D << SHIFT, in_page = pos & (c.ps - 1);
     const size_t head_bytes = (size_t)c.token_bytes() * c.ps;
     const size_t page_at = ((size_t)ap.layer * c.pages + page) * c.page_bytes();
-    for (int pass = part; pass < n; pass += kAhead * p.parts) {
+    // a pass: `now` of the token's, in slot j
+    auto put = [&](int now, int j) {
+        const int h = head_of(now);
+        const bool live = h < (now < nq ? p.q.heads : c.Hkv);
+        const bool turned = TURN && now < nq + nk && at.turned;
+        const Place &x = TURN && now < nq + nk ? at : plain;
+        if (now < nq) {
+            if (!live) return;
+            uint16_t *dst = p.q.dst + row_o + h * p.q.dl.head;
+            if (turned) {
+                float x0[8], x1[8];
+                unpack8<Q>(a[j], x0);
+                unpack8<Q>(b[j], x1);
+                turn8(x0, x1, mine, p.r.adjacent);
+                a[j] = pack8<Q>(x0);
+                b[j] = pack8<Q>(x1);
+            }
+            reinterpret_cast<uint4 *>(dst)[x.p0] = a[j];
+            reinterpret_cast<uint4 *>(dst)[x.p1] = b[j];
+            return;
+        }
+        const bool value = now >= nq + nk;
+        uint8_t *head = (value ? c.v : c.k) + page_at + h * head_bytes;
+        if constexpr (KV != kKvE2M1)
+            if (!live) return;
+        if (KV == kKv16 && !turned) {
+            reinterpret_cast<uint4 *>(head + (size_t)in_page * row_bytes)[x.p0] = a[j];
+            reinterpret_cast<uint4 *>(head + (size_t)in_page * row_bytes)[x.p1] = b[j];
+            return;
+        }
+        float x0[8], x1[8];
+        unpack8<Q>(a[j], x0);
+        unpack8<Q>(b[j], x1);
+        if (turned) turn8(x0, x1, mine, p.r.adjacent);
+        float2 scale = make_float2(1.f, 1.f);
+        if constexpr (KV != kKv16) scale = with_reciprocal(live ? __ldg((value ? c.v_scale : c.k_scale) + ap.layer * c.Hkv + h) : 1.f);
+        if constexpr (KV == kKvE2M1) {
+            put_blocks(head + (size_t)in_page * row_bytes, head + (size_t)c.ps * row_bytes + in_page * (c.D / 16), x, p.r.rot >> 4, lane, lanes, x0, x1, scale, live);
+        } else {
+            put_piece<Q, KV>(head + (size_t)in_page * row_bytes, x.p0, x0, scale);
+            put_piece<Q, KV>(head + (size_t)in_page * row_bytes, x.p1, x1, scale);
+        }
+    };
+    for (int pass = part; pass < n; pass += kAheadAppend * p.parts) {
         if (pass != part) {
 #pragma unroll
-            for (int j = 0; j < kAhead; j++) load(pass + j * p.parts, j);
+            for (int j = 0; j < kAheadAppend; j++) load(pass + j * p.parts, j);
         }
 #pragma unroll
-        for (int j = 0; j < kAhead; j++) {
-            const int now = pass + j * p.parts;
-            if (now >= n) break;
-            const int h = head_of(now);
-            const bool live = h < (now < nq ? p.q.heads : c.Hkv);
-            const bool turned = TURN && now < nq + nk && at.turned;
-            const Place &x = TURN && now < nq + nk ? at : plain;
-            if (now < nq) {
-                if (!live) continue;
-                uint16_t *dst = p.q.dst + row_o + h * p.q.dl.head;
-                if (turned) {
-                    float x0[8], x1[8];
-                    unpack8<Q>(a[j], x0);
-                    unpack8<Q>(b[j], x1);
-                    turn8(x0, x1, mine, p.r.adjacent);
-                    a[j] = pack8<Q>(x0);
-                    b[j] = pack8<Q>(x1);
-                }
-                reinterpret_cast<uint4 *>(dst)[x.p0] = a[j];
-                reinterpret_cast<uint4 *>(dst)[x.p1] = b[j];
-                continue;
-            }
-            const bool value = now >= nq + nk;
-            uint8_t *head = (value ? c.v : c.k) + page_at + h * head_bytes;
-            if constexpr (KV != kKvE2M1)
-                if (!live) continue;
-            if (KV == kKv16 && !turned) {
-                reinterpret_cast<uint4 *>(head + (size_t)in_page * row_bytes)[x.p0] = a[j];
-                reinterpret_cast<uint4 *>(head + (size_t)in_page * row_bytes)[x.p1] = b[j];
-                continue;
-            }
-            float x0[8], x1[8];
-            unpack8<Q>(a[j], x0);
-            unpack8<Q>(b[j], x1);
-            if (turned) turn8(x0, x1, mine, p.r.adjacent);
-            float2 scale = make_float2(1.f, 1.f);
-            if constexpr (KV != kKv16) scale = with_reciprocal(live ? __ldg((value ? c.v_scale : c.k_scale) + ap.layer * c.Hkv + h) : 1.f);
-            if constexpr (KV == kKvE2M1) {
-                put_blocks(head + (size_t)in_page * row_bytes, head + (size_t)c.ps * row_bytes + in_page * (c.D / 16), x, p.r.rot >> 4, lane, lanes, x0, x1, scale, live);
-            } else {
-                put_piece<Q, KV>(head + (size_t)in_page * row_bytes, x.p0, x0, scale);
-                put_piece<Q, KV>(head + (size_t)in_page * row_bytes, x.p1, x1, scale);
-            }
-        }
+        for (int j = 0; j < kAheadAppend; j++)
+            if (pass + j * p.parts < n) put(pass + j * p.parts, j);
     }
 }
 
@@ -350,7 +361,7 @@ cudaError_t launch_rope(RopeParams p, cudaStream_t stream)
     p.parts = parts_of(p.tokens, (p.x[0].heads + per - 1) / per + (p.x[1].heads + per - 1) / per, sms);
     const long long warps = (long long)p.tokens * p.parts;
     const dim3 grid((unsigned)((warps + kWarpsCta - 1) / kWarpsCta));
-    const size_t smem = (size_t)kWarpsCta * (p.r.rot / 2) * sizeof(float2);
+    const size_t smem = (size_t)kWarpsCta * p.r.rot * sizeof(float);
     return p.f16 ? launch_pdl(kda_rope_kernel<Half>, grid, dim3(kWarpsCta * 32), smem, stream, p)
                  : launch_pdl(kda_rope_kernel<Bf16>, grid, dim3(kWarpsCta * 32), smem, stream, p);
 }

@@ -144,9 +144,16 @@ def _form(out, name: str):
 
 
 def _turned(t, out, name: str, D: int, dev) -> _RopeLayout:
-    if out.shape != t.shape or out.dtype != t.dtype:
+    """Layouts of t and of its turned copy; out None: a contiguous tensor that the call makes."""
+    src = _heads(t, name, D, dev)
+    if out is None:
+        H, T = t.shape[-2], t.shape[-3]
+        dst = _Layout(src.dtype, 0 if t.dim() == 3 or t.shape[0] == 1 else T * H * D, 0 if T == 1 else H * D, 0 if H == 1 else D)
+    elif out.shape != t.shape or out.dtype != t.dtype:
         raise ValueError(f"{name}_out: {out.dtype} {tuple(out.shape)}, expected {t.dtype} {tuple(t.shape)}")
-    return _RopeLayout(t.shape[-2], _heads(t, name, D, dev), _heads(out, name + "_out", D, dev))
+    else:
+        dst = _heads(out, name + "_out", D, dev)
+    return _RopeLayout(t.shape[-2], src, dst)
 
 
 def kda_rope(rope: KdaRope, positions, q, k=None, q_out=None, k_out=None, stream=None):
@@ -158,17 +165,12 @@ def kda_rope(rope: KdaRope, positions, q, k=None, q_out=None, k_out=None, stream
     dev = q.device
     _same_device(rope, dev)
     ref = rope._struct()[1]
-    # what this module makes itself is contiguous and of the inputs' form: such calls are found by the inputs alone
     key = ("rope", dev, q.dtype, q.shape, q.stride())
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
+    if q_out is not None:
         key += ("q",) + _form(q_out, "q_out")
     if k is not None:
         key += (k.dtype, k.device, k.shape, k.stride())
-        if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        else:
+        if k_out is not None:
             key += ("k",) + _form(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -184,6 +186,11 @@ def kda_rope(rope: KdaRope, positions, q, k=None, q_out=None, k_out=None, stream
 
     tokens, D, B, T, ql, kl = _plan(rope, key, make)
     _need(positions, "positions", torch.int32, tokens, dev)
+    # outputs last: the allocator waits for what the last launch wrote to the device (a call among others 16 us, so less)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     _call(dev, _lib.kda_rope, ref, D, positions.data_ptr(), B, T, ql, q.data_ptr(), q_out.data_ptr(), kl,
           None if k is None else k.data_ptr(), None if k is None else k_out.data_ptr(), _stream(stream, dev))
     return q_out if k is None else (q_out, k_out)
@@ -204,9 +211,7 @@ def kda_kv_append_rope(cache: KdaKvCache, layer: int, rows, rope: KdaRope, q, k,
     key = ("append_rope", B, cu_seqlens is None, k.dtype, v.dtype, k.device, v.device, k.shape, v.shape, k.stride(), v.stride())
     if q is not None:
         key += (q.dtype, q.device, q.shape, q.stride())
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        else:
+        if q_out is not None:
             key += _form(q_out, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -240,6 +245,8 @@ def kda_kv_append_rope(cache: KdaKvCache, layer: int, rows, rope: KdaRope, q, k,
     T, ql, kl, vl = _plan(cache, key, make)
     pc = None if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", B + 1, dev)
     pn = None if n_tokens is None else _ints(n_tokens, "n_tokens", B, dev)
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     _call(dev, _lib.kda_kv_append_rope, st, _i32(layer, "layer"), ref, pr, B, T, pn, pc, ql, None if q is None else q.data_ptr(),
           None if q is None else q_out.data_ptr(), k.data_ptr(), kl, v.data_ptr(), vl, _stream(stream, dev))
     return q_out
