@@ -1,6 +1,7 @@
 """A small hybrid model served end to end: KDA mixer layers with softmax-attention layers between them.
 
-Random weights; the point is how the calls go together.  Two prompts are prefilled in one packed call,
+Random weights; the point is how the calls go together.  The attention layers may rotate queries and keys by their
+positions (on the keys' way into the cache), and the cache may hold 16, 8 or 4 bits.  Two prompts are prefilled in one packed call,
 each is forked into two samples, the samples decode token by token, then verify drafts of which some
 are accepted, and finish: their pages are given back and the cache is closed up.  At the end every
 sample's tokens are run again as one prompt, and the two ways have to agree.
@@ -22,9 +23,11 @@ BF = torch.bfloat16
 
 
 class Hybrid:
-    """`kinds`: "kda" for a KDA mixer layer, a window (0 = none) for a softmax-attention layer."""
+    """`kinds`: "kda" for a KDA mixer layer, a window (0 = none) for a softmax-attention layer; `rotary_dim`: elements of a head
+    that the attention layers rotate (0: none)."""
 
-    def __init__(self, kinds=("kda", 0, "kda", 64), width=256, H=2, Hq=4, Hkv=2, D=64, seed=0, rows=16, pages=64, ps=16, cache_dtype=BF):
+    def __init__(self, kinds=("kda", 0, "kda", 64), width=256, H=2, Hq=4, Hkv=2, D=64, seed=0, rows=16, pages=64, ps=16, cache_dtype=BF,
+                 rotary_dim=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         w = lambda *s, std=None: (torch.randn(*s, device="cuda", generator=g) * (std or s[0] ** -0.5)).to(BF)
         self.kinds, self.width, self.H, self.Hq, self.Hkv, self.D = kinds, width, H, Hq, Hkv, D
@@ -43,6 +46,7 @@ class Hybrid:
         if cache_dtype == torch.float8_e4m3fn:
             self.cache.k_scale.fill_(0.02)
             self.cache.v_scale.fill_(0.02)
+        self.rope = K.KdaRope.make(rotary_dim, scaling="yarn", factor=4.0, original_len=64) if rotary_dim else None
 
     def _norm(self, x):
         return torch.nn.functional.rms_norm(x.float(), (self.width,)).to(BF)
@@ -64,13 +68,20 @@ class Hybrid:
             x = x + o @ w_out
         return x
 
+    def _append(self, layer, rows, q, k, v, cu=None):
+        """New keys and values into the cache; returns the queries that attend."""
+        if self.rope is None:
+            K.kda_kv_append(self.cache, layer, rows, k, v, cu_seqlens=cu)
+            return q
+        return K.kda_kv_append_rope(self.cache, layer, rows, self.rope, q, k, v, cu_seqlens=cu)
+
     def prefill(self, x, rows, cu, lens):
         """Packed prompts x [tokens, width], sequence b in row rows[b]."""
         n = torch.tensor(lens, dtype=torch.int32, device="cuda")
         K.kda_kv_extend(self.cache, rows, n)
 
         def attn(layer, q, k, v, window):
-            K.kda_kv_append(self.cache, layer, rows, k, v, cu_seqlens=cu)
+            q = self._append(layer, rows, q, k, v, cu)
             return K.kda_attn_prefill(self.cache, layer, rows, cu, max(lens), q, window=window, sinks=4)
 
         return self._run(x, rows, lambda la, p, r, *i: K.kda_prefill_varlen(la, p, r, cu, max(lens), *i), attn)
@@ -78,7 +89,7 @@ class Hybrid:
     def _attn_step(self, rows):
         def attn(layer, q, k, v, window):
             q, k, v = (t if t.dim() == 4 else t[:, None] for t in (q, k, v))
-            K.kda_kv_append(self.cache, layer, rows, k, v)
+            q = self._append(layer, rows, q, k, v)
             return K.kda_attn_decode(self.cache, layer, rows, q, window=window, sinks=4)
 
         return attn
@@ -171,5 +182,6 @@ def serve(model, seed=1, lens=(37, 70), steps=5, T=4):
 
 
 if __name__ == "__main__":
-    for name, dtype in (("bfloat16", BF), ("E4M3", torch.float8_e4m3fn)):
-        print("%s cache: step by step against one prompt, largest difference %.2g of the largest output" % (name, serve(Hybrid(cache_dtype=dtype))))
+    for name, kw in (("bfloat16", dict()), ("E4M3", dict(cache_dtype=torch.float8_e4m3fn)), ("bfloat16, rotated", dict(rotary_dim=32)),
+                     ("4-bit, rotated", dict(cache_dtype=torch.uint8, rotary_dim=64))):
+        print("%s cache: step by step against one prompt, largest difference %.2g of the largest output" % (name, serve(Hybrid(**kw))))
