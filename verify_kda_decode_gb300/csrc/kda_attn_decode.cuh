@@ -20,6 +20,11 @@
 //
 // Rows of a page that no token sees are not read: cp.async writes zeros for them, so whatever the
 // page holds there (NaN included) cannot reach the products.
+//
+// 4-bit caches (E2M1 codes, an E4M3 scale for each 16 elements of a key): bytes halve again and the instructions do not.  Two codes a
+// conversion and a product with their scale, both exact in halves, are 256 of about 630 instructions for 32 keys of 128 dims and a
+// block of 8 rows; in long runs HBM bounds it all the same (608 sequences of 32768 tokens: 5.8 TB/s), in short units their
+// starts and merges do (256 sequences of 1 to 4096 tokens, 8 heads: 120 us, 4.4 TB/s).
 #pragma once
 
 #include "kda_attn_common.cuh"

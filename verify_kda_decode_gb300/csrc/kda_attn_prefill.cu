@@ -18,7 +18,7 @@
 //
 // Roles: warps 0-3 and 4-7 are the softmax of the two halves (one thread per row), warps 8-11 copy
 // keys and values into a ring of shared-memory tiles, warp 12 issues every MMA, warp 13 finds
-// the next unit (14 and 15 only give their registers away).  Hand-over
+// the next unit (14 and 15 only give their registers away; with a 4-bit cache 14 fetches codes).  Hand-over
 // by mbarriers; a half's S tile also orders its previous P V (a commit covers every MMA issued before
 // it).  With few row tiles the key tiles are split over several CTAs whose partial (m, l, O) the last
 // one to finish joins in a fixed order.
@@ -32,6 +32,13 @@
 // codes on their way.  Keys that are seen but whose table entry names no page come as zeros too, and the loaders
 // leave the softmax a word for each tile that says which groups of 8 keys these are (4 x 4096 tokens 395.2 -> 397.7 us; with
 // the pages looked up beside the sums 402 to 414).
+//
+// 4-bit caches: a code times its block's E4M3 scale is exact in a half (two significant bits by four, 2^-10 to 2688), so the tiles are
+// halves, converted from 72 bytes a key of 128 dims.  Warp 14 brings whole pages' bytes by bulk copies and warps 8-11 only convert;
+// bfloat16 queries come by TMA and are brought to halves in place by the softmax's threads.  4 x 4096 tokens, 32/8 heads: 510 us
+// (16-bit caches 395).  As with E4M3 codes, the four warps looking up, fetching and converting, 824 us: a fetch took 1350 clocks
+// beside a conversion of 650; with addresses once a tile 738; bulk copies 536.  Without the conversion's instructions 450: they
+// share the issue slots and shared memory with the softmax, and neither waits long for the other.
 #include <cuda.h>
 
 #include "kda_attn_common.cuh"
@@ -508,7 +515,9 @@ __device__ bool load_unit(Smem<D, KV> &sm, const Args &args, const Unit &u, int 
             }
         }
     } else if constexpr (KV == kKvE2M1) {
-        // Warp 14 fetches the codes (fetch_unit); these warps only convert them, 32 keys each.
+        // Warp 14 fetches the codes (fetch_unit); these warps only convert them, 32 keys each.  (Two warps for keys and two for
+        // values, with twice the items on their way: 620 us against 510; a ring of four tiles with two or three fetches
+        // ahead, or three tiles with five: within 2 % or slower.)
         constexpr int ROWS = 32 / CPR;   // a pass: chunk cp of ROWS keys
         const int row = lane % ROWS, cp = lane / ROWS, at_codes = (w * 32 + row) * RB + cp * 16, at_scales = (w * 32 + row) * SB + 2 * cp;
         int at_tile[4];   // (the rows of later passes are whole groups of 8 further: the same places in their swizzle)
