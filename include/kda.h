@@ -391,7 +391,8 @@ kda_status kda_kv_append(const kda_kv_cache *cache, int32_t layer, const int32_t
  * product of position and frequency is taken modulo 2^64, so the angle keeps its precision (2^-24 of
  * a turn) at any position; a negative position turns back.  The products are FP32, rounded once. */
 typedef struct {
-    const uint64_t *turns;   /* [rotary_dim / 2] (device): turns per position, in units of 2^-64 */
+    const uint64_t *turns;   /* [rotary_dim / 2] (device, 8-byte aligned): turns per position, in units
+                                of 2^-64 */
     int32_t rotary_dim;      /* a multiple of 16, at most the head dim */
     int32_t interleaved;     /* 0 or 1 */
     float scale;             /* finite; 1 unless the scaling asks for another */

@@ -130,7 +130,9 @@ struct Cfg {
     // CTAs of an SM: as many as the accumulators (D NB / 4 registers) leave room for.  A warp's step is a
     // chain of latencies (scores, exponentials, product), which other warps cover: two CTAs everywhere
     // against this, 64 x 4096 tokens, 8 heads, E4M3: 153 us, 129 us; bfloat16 (HBM bound) 171 us both.
-    static constexpr int OCC = D * NB >= 512 ? 2 : (RB == 256 || D * NB >= 256) ? 3 : 4;
+    // 4-bit blocks of 24 rows one fewer: with more they spill (20 rows, 64 x 4096 tokens, 8 heads: 131 us, 122 of 128 dims, 84 and 76
+    // of 64; in a 1024 window, a unit a CTA, 30.2 and 31.2).
+    static constexpr int OCC = D * NB >= 512 ? 2 : KV == kKvE2M1 && NB == 3 ? (D == 64 ? 3 : 2) : (RB == 256 || D * NB >= 256) ? 3 : 4;
     static constexpr bool Q_SMEM = NB > 1;                // queries in shared memory instead of registers
     static constexpr int Q_BYTES = Q_SMEM ? NB * 8 * D * 2 : 0;
     // Sequences whose (row, length, tokens) are kept on chip.  E2M1: three stages and four CTAs take all of the 228 KB but 2 KB a CTA.

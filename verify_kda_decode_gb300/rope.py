@@ -186,7 +186,7 @@ def kda_rope(rope: KdaRope, positions, q, k=None, q_out=None, k_out=None, stream
 
     tokens, D, B, T, ql, kl = _plan(rope, key, make)
     _need(positions, "positions", torch.int32, tokens, dev)
-    # outputs last: the allocator waits for what the last launch wrote to the device (a call among others 16 us, so less)
+    # outputs last: an allocation right behind the last call's launch waits for it (a call of one token 16.3 us, like this 13.8)
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k is not None and k_out is None:
