@@ -18,10 +18,10 @@ namespace kda {
 namespace {
 
 constexpr int kWarpsCta = 8;
-// Heads of a lane whose pieces are on their way at once.  The rotation alone: two, each followed by the next one's load, in 24 warps
-// an SM (4 x 4096 tokens 55.6 us; three 57.2, four in 16 warps 59); the append: four at a time in 16 warps (32000 tokens to E4M3
-// 142 us; one by one 148, two in 24 warps 145).
-constexpr int kAhead = 2, kAheadAppend = 4;
+// Heads of a lane whose pieces are on their way at once: two, in 24 warps an SM.  The rotation alone, each head followed by the next
+// one's load: 4 x 4096 tokens 55.7 us (three 57.2, four in 16 warps 59).  The append, two at a time: 32000 tokens, queries kept,
+// keys and values to E4M3 143 us (one in 32 warps 155, four in 16 warps 146), to 4 bits 171 us (176, 180).
+constexpr int kAhead = 2;
 
 template <typename Q>
 __device__ __forceinline__ void unpack8(const uint4 &w, float *x)
@@ -56,17 +56,19 @@ struct Place {
     }
 };
 
-// Cosines, then sines, of the angles of a position, by the warp, in its shared memory.
+// Cosine and sine of angle f of a position to their places in the warp's shared memory (cosines, then sines).
+__device__ __forceinline__ void angle(const Turns &r, int pos, unsigned long long freq, int f, float *cs)
+{
+    const long long turn = (long long)((unsigned long long)(long long)pos * freq);
+    float s, c;
+    sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
+    cs[f] = c * r.scale;
+    cs[r.rot / 2 + f] = s * r.scale;
+}
+// All angles of a position, by the warp.
 __device__ __forceinline__ void angles(const Turns &r, int pos, float *cs, int lane)
 {
-    const int n = r.rot / 2;
-    for (int f = lane; f < n; f += 32) {
-        const long long turn = (long long)((unsigned long long)(long long)pos * __ldg(r.freq + f));
-        float s, c;
-        sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
-        cs[f] = c * r.scale;
-        cs[n + f] = s * r.scale;
-    }
+    for (int f = lane; f < r.rot / 2; f += 32) angle(r, pos, __ldg(r.freq + f), f, cs);
     __syncwarp();
 }
 
@@ -227,7 +229,7 @@ __device__ __forceinline__ void put_blocks(uint8_t *codes, uint8_t *scales, cons
 
 // A warp for a token (or a part of its heads): queries turned into p.q.dst, keys turned into their page, values into theirs.
 template <typename Q, int KV, bool TURN>
-__global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(const AppendTurnParams p)
+__global__ void __launch_bounds__(kWarpsCta * 32, 3) kda_kv_append_turn_kernel(const AppendTurnParams p)
 {
     __shared__ __align__(16) float all_angles[kWarpsCta][TURN ? 128 : 4];
     const AppendParams &ap = p.a;
@@ -245,7 +247,8 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(cons
     const long long seq = ap.cu ? 0 : tok / ap.T, in_seq = tok - seq * ap.T;
     const long long row_k = (ap.cu ? 0 : seq * ap.kl.seq) + in_seq * ap.kl.token, row_v = (ap.cu ? 0 : seq * ap.vl.seq) + in_seq * ap.vl.token;
     const long long row_q = (ap.cu ? 0 : seq * p.q.sl.seq) + in_seq * p.q.sl.token, row_o = (ap.cu ? 0 : seq * p.q.dl.seq) + in_seq * p.q.dl.token;
-    uint4 a[kAheadAppend], b[kAheadAppend];
+    uint4 a[kAhead], b[kAhead];
+    [[maybe_unused]] float layer_scale[kAhead];
     // pass: heads of the queries, then of the keys, then of the values
     auto head_of = [&](int pass) { return (pass < nq ? pass : pass < nq + nk ? pass - nq : pass - nq - nk) * per + mine_h; };
     auto load = [&](int pass, int j) {
@@ -254,17 +257,28 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(cons
         if (h >= (pass < nq ? p.q.heads : c.Hkv)) return;
         const uint16_t *src = pass < nq ? p.q.src + row_q + h * p.q.sl.head : pass < nq + nk ? ap.k + row_k + h * ap.kl.head : ap.v + row_v + h * ap.vl.head;
         const Place &x = TURN && pass < nq + nk ? at : plain;
+        if constexpr (KV != kKv16)
+            if (pass >= nq) layer_scale[j] = __ldg((pass < nq + nk ? c.k_scale : c.v_scale) + ap.layer * c.Hkv + h);
         a[j] = __ldcs(reinterpret_cast<const uint4 *>(src) + x.p0);
         b[j] = __ldcs(reinterpret_cast<const uint4 *>(src) + x.p1);
     };
-    // the first pieces are on their way while the token's place is found
+    // the first pieces, and the frequencies, are on their way while the token's place is found
 #pragma unroll
-    for (int j = 0; j < kAheadAppend; j++) load(part + j * p.parts, j);
+    for (int j = 0; j < kAhead; j++) load(part + j * p.parts, j);
+    unsigned long long freq[2] = {};   // (a cache's heads have 64 pairs at most)
+    if constexpr (TURN) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (lane + 32 * i < p.r.rot / 2) freq[i] = __ldg(p.r.freq + lane + 32 * i);
+    }
     int pos, page;
     if (!append_place(ap, tok, seq, in_seq, lane, lane == 0 && part == 0, pos, page)) return;
     [[maybe_unused]] Angles mine;
     if constexpr (TURN) {
-        angles(p.r, pos, all_angles[warp], lane);
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (lane + 32 * i < p.r.rot / 2) angle(p.r, pos, freq[i], lane + 32 * i, all_angles[warp]);
+        __syncwarp();
         if (at.turned) load_angles(p.r, all_angles[warp], u, mine);
     }
     constexpr int SHIFT = KV == kKv16 ? 1 : 0;
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(cons
         unpack8<Q>(b[j], x1);
         if (turned) turn8(x0, x1, mine, p.r.adjacent);
         float2 scale = make_float2(1.f, 1.f);
-        if constexpr (KV != kKv16) scale = with_reciprocal(live ? __ldg((value ? c.v_scale : c.k_scale) + ap.layer * c.Hkv + h) : 1.f);
+        if constexpr (KV != kKv16) scale = with_reciprocal(live ? layer_scale[j] : 1.f);
         if constexpr (KV == kKvE2M1) {
             put_blocks(head + (size_t)in_page * row_bytes, head + (size_t)c.ps * row_bytes + in_page * (c.D / 16), x, p.r.rot >> 4, lane, lanes, x0, x1, scale, live);
         } else {
@@ -314,13 +328,13 @@ __global__ void __launch_bounds__(kWarpsCta * 32) kda_kv_append_turn_kernel(cons
             put_piece<Q, KV>(head + (size_t)in_page * row_bytes, x.p1, x1, scale);
         }
     };
-    for (int pass = part; pass < n; pass += kAheadAppend * p.parts) {
+    for (int pass = part; pass < n; pass += kAhead * p.parts) {
         if (pass != part) {
 #pragma unroll
-            for (int j = 0; j < kAheadAppend; j++) load(pass + j * p.parts, j);
+            for (int j = 0; j < kAhead; j++) load(pass + j * p.parts, j);
         }
 #pragma unroll
-        for (int j = 0; j < kAheadAppend; j++)
+        for (int j = 0; j < kAhead; j++)
             if (pass + j * p.parts < n) put(pass + j * p.parts, j);
     }
 }
