@@ -649,8 +649,12 @@ __device__ bool fetch_unit(Smem<D, kKvE2M1> &sm, const Args &args, const Unit &u
             uint64_t *bar = &sm.raw_full[to];
             const ptrdiff_t add = kv ? v_minus_k : 0;
             if (ring >= SM::kRaw && !wait_warp(sm, &sm.raw_empty[to], (ring / SM::kRaw - 1) & 1, c.err)) return false;
-            // (told ahead of the tile's keys, see tell_gone: its raw item has waited for the conversion of the one kRaw items before)
-            if (kv == 0 && lane == 0) sm.gone[(ring >> 1) % kGone] = gone;
+            // (told ahead of the tile's keys, see tell_gone: its raw item has waited for the conversion of the one kRaw items before;
+            // the plain arrival releases the word, which an arrival by asynchronous copies does not)
+            if (lane == 0) {
+                if (kv == 0) sm.gone[(ring >> 1) % kGone] = gone;
+                mbar_arrive(bar);
+            }
             if (whole) {
                 if (written >> to & 1) {   // before a bulk copy overwrites what these lanes' copies wrote
                     tc::fence_smem_to_async();
@@ -1154,7 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const __g
         mbar_init(&sm.drain, 1);
         mbar_init(&sm.q_raw, 1);
         for (int i = 0; i < Smem<D, KV>::kRaw; i++) {
-            mbar_init(&sm.raw_full[i], 32);
+            mbar_init(&sm.raw_full[i], 33);   // lane 0 of warp 14, and its lanes or their copies
             mbar_init(&sm.raw_empty[i], kLoaders / 32);
         }
         for (int i = 0; i < (int)Smem<D, KV>::kSlots; i++) {
