@@ -54,7 +54,7 @@ class KdaRope:
         """Frequencies base^(-2 i / rotary_dim), scaled for contexts `factor` times as long as trained:
         None; "linear" (positions divided by factor); "ntk" (a larger base, the slowest pair divided by factor); "yarn" (pairs
         that turn less than beta_slow times in original_len positions divided by factor, those above beta_fast kept, a ramp
-        over the pairs between, and everything multiplied by 0.1 ln(factor) + 1)."""
+        over the pairs between, and everything multiplied by 0.1 ln(factor) + 1; beta_slow is at most beta_fast)."""
         if rotary_dim < 2 or rotary_dim % 2:
             raise ValueError(f"rotary_dim={rotary_dim} must be even")
         if not (factor > 0 and math.isfinite(factor) and base > 1 and math.isfinite(base)):
@@ -68,14 +68,16 @@ class KdaRope:
         if scaling == "linear":
             f = [x / factor for x in f]
         elif scaling == "yarn":
-            if not (original_len > 0 and beta_fast > 0 and beta_slow > 0):
-                raise ValueError(f"original_len={original_len}, beta_fast={beta_fast}, beta_slow={beta_slow}: each must be positive")
+            if not (0 < original_len < math.inf and 0 < beta_slow <= beta_fast < math.inf):
+                raise ValueError(f"original_len={original_len}, beta_fast={beta_fast}, beta_slow={beta_slow}: each must be positive and finite, beta_slow at most beta_fast")
 
             def pair(turns):   # (fractional) pair that turns so many times
                 return rotary_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
 
             lo, hi = max(0, math.floor(pair(beta_fast))), min(rotary_dim - 1, math.ceil(pair(beta_slow)))
             keep = [1.0 - min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(rotary_dim // 2)]
+            if pair(beta_slow) < 0:   # no pair turns so often: the ramp, which begins at pair 0 at the earliest, has no place
+                keep = [0.0] * len(keep)
             f = [x * k + x / factor * (1.0 - k) for x, k in zip(f, keep)]
             scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
         elif scaling not in (None, "ntk"):
