@@ -173,8 +173,15 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+class _Copies:
+    """Copies and pickles take the fields.  What was built of them (names with a leading underscore) holds addresses and stays behind."""
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
+
+
 @dataclass
-class KdaLayer:
+class KdaLayer(_Copies):
     """Weights of one KDA layer on the device (see kda_layer in include/kda.h).  W_fb is bf16,
     or float8_e4m3fn codes with W_fb_scale (f32 [H*128], one scale per row): the FP8 path."""
     W_fb: torch.Tensor      # bf16 or float8_e4m3fn [H*128, 128]
@@ -223,7 +230,7 @@ class KdaLayer:
 
 
 @dataclass
-class KdaPool:
+class KdaPool(_Copies):
     """Caller-owned slot pool (see kda_pool in include/kda.h)."""
     state: torch.Tensor        # f32 or bf16 [num_slots, H, 128, 128]
     conv_state: torch.Tensor   # bf16 [num_slots, 3, 3, H*128]

@@ -17,7 +17,8 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from .kda import (KDA_DEVERR_TIMEOUT, KDA_ERR_DEVICE, KDA_OK, KDA_T_BF16, KDA_T_E2M1, KDA_T_E4M3, KDA_T_F16, _call, _lib, _need, _ptr, _raise, _stream)
+from .kda import (KDA_DEVERR_TIMEOUT, KDA_ERR_DEVICE, KDA_OK, KDA_T_BF16, KDA_T_E2M1, KDA_T_E4M3, KDA_T_F16, _call, _Copies, _lib, _need, _ptr, _raise,
+                  _stream)
 
 # of a cache; uint8 is the storage of a 4-bit one
 _TYPES = {torch.bfloat16: KDA_T_BF16, torch.float16: KDA_T_F16, torch.float8_e4m3fn: KDA_T_E4M3, torch.uint8: KDA_T_E2M1}
@@ -46,7 +47,7 @@ class _Desc(ctypes.Structure):
 
 
 @dataclass
-class KdaKvCache:
+class KdaKvCache(_Copies):
     """Caller-owned paged cache (see kda_kv_cache in include/kda.h).
 
     A 4-bit cache (E2M1 codes with an E4M3 scale for each 16 elements) is held as uint8 [layers, pages, Hkv, page size,
@@ -64,6 +65,10 @@ class KdaKvCache:
         if self.err_word is None:
             self.err_word = torch.zeros(1, dtype=torch.int32, device=self.k.device)
         self._make_workspaces()
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._make_workspaces()   # a copy's own, as a new cache's
 
     @staticmethod
     def zeros(layers: int, num_pages: int, Hkv: int, rows: int, max_pages: int, page_size: int = 64,

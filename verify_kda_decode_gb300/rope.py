@@ -14,7 +14,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from .kda import _call, _lib, _need, _ptr, _stream
+from .kda import _call, _Copies, _lib, _need, _ptr, _stream
 from .paged import _TYPES, KdaKvCache, _i32, _ints, _Layout, _plan, _rows, _tokens
 
 _PI = Fraction(3141592653589793238462643383279502884197169399375106, 10 ** 51)
@@ -29,7 +29,7 @@ class _RopeLayout(ctypes.Structure):
 
 
 @dataclass
-class KdaRope:
+class KdaRope(_Copies):
     """How positions turn the pairs of a head (see kda_rope_desc in include/kda.h)."""
     turns: torch.Tensor        # int64 [rotary_dim / 2]: turns per position, in units of 2^-64 (modulo 2^64)
     interleaved: bool = False  # pairs (2 i, 2 i + 1) instead of (i, i + rotary_dim / 2)
