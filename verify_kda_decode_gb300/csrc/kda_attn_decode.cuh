@@ -62,18 +62,12 @@ __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// ... from zero
-template <typename T>
+// ... of halves, from zero
 __device__ __forceinline__ void mma16816_zero(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
 {
-    if constexpr (T::is_half)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Transposes an 8x8 matrix of 16-bit elements held one row per quad.
@@ -182,13 +176,6 @@ __device__ __forceinline__ void cp16(uint32_t dst, const uint8_t *src)
 __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const uint8_t *src, bool read)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
-}
-
-// N (4 or 8) bytes
-template <int N>
-__device__ __forceinline__ void cp_scales(uint32_t dst, const uint8_t *src, bool read)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(read ? N : 0) : "memory");
 }
 
 // Runs of tiles are counted in 64 bits (rows that share pages can hold more keys than memory); the
@@ -479,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
                     cp16_or_zero(dst + C::V_AT + dst_v + i * 512, src + v_minus_k, read);
                 }
                 const int r = lane % kStep, j = g0 + r;   // block scales: half the lanes keys', the others values'
-                cp_scales<C::SB>(to + (lane < kStep ? C::KS_AT : C::VS_AT) + (sub * kStep + r) * C::SB,
-                                 head + (lane < kStep ? 0 : v_minus_k) + (size_t)c.ps * C::RB + (row0 + r) * C::SB,
-                                 ok && j < kr.end && (j >= kr.lo || j < S));
+                cp_async_small<C::SB>(to + (lane < kStep ? C::KS_AT : C::VS_AT) + (sub * kStep + r) * C::SB,
+                                      head + (lane < kStep ? 0 : v_minus_k) + (size_t)c.ps * C::RB + (row0 + r) * C::SB,
+                                      ok && j < kr.end && (j >= kr.lo || j < S) ? C::SB : 0);
             }
         };
         auto issue = [&](int t, int stage) {
@@ -571,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
                             uint2 q;
                             if constexpr (C::Q_SMEM) q = lds64(q_at + (nb * (D / 16) + 2 * u + i) * 256);
                             else q = make_uint2(qf[2 * u + i][0], qf[2 * u + i][1]);
-                            if (u == 0 && i == 0) mma16816_zero<P>(s[sub][nb], a, q.x, q.y);
+                            if (u == 0 && i == 0) mma16816_zero(s[sub][nb], a, q.x, q.y);
                             else mma16816<P>(s[sub][nb], a, q.x, q.y);
                         }
                     }

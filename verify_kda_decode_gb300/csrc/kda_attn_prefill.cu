@@ -685,7 +685,7 @@ __device__ bool fetch_unit(Smem<D, kKvE2M1> &sm, const Args &args, const Unit &u
                 }
                 for (int r = lane; r < kKeys; r += 32) {
                     const uint8_t *h = key(r);
-                    cp_async_small<SB>(sm.raw_scale[to] + r * SB, h ? h + (size_t)c.ps * RB + ((k0 + r) & (c.ps - 1)) * SB : c.k, h ? SB : 0);
+                    cp_async_small<SB>(smem_u32(sm.raw_scale[to] + r * SB), h ? h + (size_t)c.ps * RB + ((k0 + r) & (c.ps - 1)) * SB : c.k, h ? SB : 0);
                 }
                 written |= 1u << to;
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");

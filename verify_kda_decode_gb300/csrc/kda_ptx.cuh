@@ -90,12 +90,12 @@ __device__ __forceinline__ void cp_async16(void *smem_dst, const void *gmem_src,
                  ::"r"(smem_u32(smem_dst)), "l"(gmem_src), "r"(src_bytes) : "memory");
 }
 
-// ... of N (4 or 8) bytes.
+// ... of N (4 or 8) bytes, to a shared address.
 template <int N>
-__device__ __forceinline__ void cp_async_small(void *smem_dst, const void *gmem_src, uint32_t src_bytes)
+__device__ __forceinline__ void cp_async_small(uint32_t smem_dst, const void *gmem_src, uint32_t src_bytes)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
-                 ::"r"(smem_u32(smem_dst)), "l"(gmem_src), "n"(N), "r"(src_bytes) : "memory");
+                 ::"r"(smem_dst), "l"(gmem_src), "n"(N), "r"(src_bytes) : "memory");
 }
 
 // Waits until this thread's cp_async16 copies have landed in shared memory.
