@@ -41,13 +41,19 @@ constexpr int kUnitRows = 32;
 // sequences, four drafts, 1024 window: 70 us, with 2 / 4 / 8: 47 / 41 / 41 us; 131072 tokens of one
 // sequence: 91 us, 90 / 89 / 94 us.
 constexpr int kUnitCost = 4;
-// How many places longer a run may get for whole units to each CTA (see where the runs are made); two numbers for all forms.
-// Measured both ways on 44 forms (16-bit and E4M3 caches, 64 and 128 dims, 1 to 100 sequences of 300 to 2048 tokens, 32
+// How many places longer a run may get for whole units to each CTA (see where the runs are made): Cfg::UNEVEN, or kUnevenShort
+// where the runs are shorter than a unit's start.  A place is a tile, 64 keys of a 16-bit or E4M3 cache and 128 of a 4-bit one.
+// 16 bits and E4M3, 12 and 8: measured both ways on 44 forms (64 and 128 dims, 1 to 100 sequences of 300 to 2048 tokens, 32
 // query and 8 key heads, one and four tokens): the 22 that get whole units gain 1 to 38 % by them, but for two that lose
 // 1.5 %; of the 22 that are cut, whole units would cost 17 forms 1 to 23 % (one sequence of 517 tokens, 12 places more: 8.5
 // us cut, 10.2 whole; of 300 tokens, 8 more: 9.2 and 7.7) and would gain five of 64 dims 2 to 16 %.  64 ragged sequences in a
 // 1024 window, 20 rows a unit: 35.3 us with cut units, 31.1 with whole ones (9 more).
-constexpr int kUneven = 12, kUnevenShort = 8;
+// 4 bits, 7 and 8: measured both ways on 208 forms (64 and 128 dims, 1 to 152 sequences of 300 to 8192 tokens, windows of 512 to
+// 2048, 8 key heads, 4 to 32 rows).  Longer runs: whole units of 1 to 7 places more take 1 to 43 % less time than cut ones, of 8
+// and 9 from 9 % less to 20 % more, of 10 and above 4 to 48 % more (64 sequences of 1024 tokens, 16 rows, 10 more: 40.3 us cut,
+// 45.2 whole; but three units of 15 places for a run of 37: 83 us cut, 77 whole).  Short runs: of 8 at most from 37 % less (four sequences of 517 tokens, 32 rows: 32.6 us cut, 20.5 whole) to 15 %
+// more, of 9 and above from 12 % less to 131 % more.
+constexpr int kUnevenShort = 8;
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
@@ -149,6 +155,7 @@ struct Cfg {
         return D == 128 ? (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (2 * ((r >> 1) & 3))) * 16)
                         : (r >> 2) * 128 + ((((r & 3) * 2 + c) ^ (2 * ((r >> 2) & 1))) * 16);
     }
+    static constexpr int UNEVEN = KV == kKvE2M1 ? 7 : 12;   // see kUnevenShort
     // head dim of the first of the two elements that accumulator block m of lane group g holds
     static __device__ __forceinline__ int dim(int m, int g) { return KV != kKv16 ? (D / 8) * g + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3); }
 };
@@ -257,11 +264,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KV, NB>::OCC) kda_attn_decode
         most = max(most, sh_most[i]);
     }
     long long chunk = max(1ll, div_pos(total + gridDim.x - 1, gridDim.x));
-    // Whole units to each CTA, places as many as the longest unit has, where the longest run gets no more than kUneven
+    // Whole units to each CTA, places as many as the longest unit has, where the longest run gets no more than C::UNEVEN
     // places longer (kUnevenShort, where the runs are shorter than a unit's start): no unit is started twice and none
     // is joined.
     const int each = all_units <= (int)gridDim.x ? 1 : (all_units + gridDim.x - 1) / gridDim.x;
-    if (all_units < 1 << 20 && (long long)each * most <= chunk + (chunk > kUnitCost ? kUneven : kUnevenShort)) {
+    if (all_units < 1 << 20 && (long long)each * most <= chunk + (chunk > kUnitCost ? C::UNEVEN : kUnevenShort)) {
         int x = units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
