@@ -94,7 +94,7 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
 // What scores are multiplied with: 0 as the least that keeps hidden scores at -inf.  A NaN (of a scale in the cache) stays one.
 __device__ __forceinline__ float score_scale(float x) { return x < 1e-37f ? 1e-37f : x; }
 
-// With an E4M3 cache the products are taken in halves.  A bfloat16 row of queries is brought to a maximum in
+// With a cache of codes (E4M3, E2M1) the products are taken in halves.  A bfloat16 row of queries is brought to a maximum in
 // [1, 2) by a power of two first (exact but for elements under 2^-14 of it, whose error stays under 2^-25 of
 // it): `mag` is the row's largest magnitude's bits; returns the factor `down` for the elements and `up` for
 // the scores.  Rows with infinities or NaN stay as they are.

@@ -12,7 +12,8 @@
 // Bound.  Every key and value byte is used for R rows only: HBM bound (R <= 32 needs at most 1/8 of
 // the tensor rate).  So the design is about bytes in flight and an even split.  Each warp owns a ring
 // of cp.async stages (16 keys and values a stage; two to four stages, 12 to 24 KiB a warp, 8 to 16 warps and
-// 144 to 192 KiB an SM, see Cfg, against about 45 KiB that the latency-bandwidth product asks of an SM), with no
+// 144 to 192 KiB an SM, see Cfg, against about 45 KiB that the latency-bandwidth product asks of an SM; with 4 bits 32 keys and
+// values a stage, three to six stages, 11 to 23 KiB a warp and 162 to 216 KiB an SM), with no
 // CTA barrier inside a run of keys.  All tiles of all (sequence, key head, row block) units are laid out in one line and
 // cut into equal runs, one per CTA, so ragged lengths load the SMs evenly; a unit that spans several
 // CTAs leaves partial (m, l, O) in the workspace and the CTA that finishes last joins them in the
@@ -24,7 +25,9 @@
 // 4-bit caches (E2M1 codes, an E4M3 scale for each 16 elements of a key): bytes halve again and the instructions do not.  Two codes a
 // conversion and a product with their scale, both exact in halves, are 256 of about 630 instructions for 32 keys of 128 dims and a
 // block of 8 rows; in long runs HBM bounds it all the same (608 sequences of 32768 tokens: 5.8 TB/s), in short units their
-// starts and merges do (256 sequences of 1 to 4096 tokens, 8 heads: 120 us, 4.4 TB/s).
+// starts and merges do (256 sequences of 1 to 4096 tokens, 8 heads: 120 us, 4.4 TB/s).  With more rows latencies do, at 8 to 12 warps an
+// SM: 64 x 4096 tokens, 20 rows 119 us, 32 rows 149 (issue slots 40 % busy; these blocks spill 84 bytes of loads a thread, with half
+// queries 252: 178 us; of 64 dims 100 and 28: 95 and 91 us).
 #pragma once
 
 #include "kda_attn_common.cuh"
@@ -51,8 +54,8 @@ constexpr int kUnitCost = 4;
 // 4 bits, 7 and 8: measured both ways on 208 forms (64 and 128 dims, 1 to 152 sequences of 300 to 8192 tokens, windows of 512 to
 // 2048, 8 key heads, 4 to 32 rows).  Longer runs: whole units of 1 to 7 places more take 1 to 43 % less time than cut ones, of 8
 // and 9 from 9 % less to 20 % more, of 10 and above 4 to 48 % more (64 sequences of 1024 tokens, 16 rows, 10 more: 40.3 us cut,
-// 45.2 whole; but three units of 15 places for a run of 37: 83 us cut, 77 whole).  Short runs: of 8 at most from 37 % less (four sequences of 517 tokens, 32 rows: 32.6 us cut, 20.5 whole) to 15 %
-// more, of 9 and above from 12 % less to 131 % more.
+// 45.2 whole; but three units of 15 places for a run of 37: 83 us cut, 77 whole).  Short runs: of 8 at most from 37 % less (four
+// sequences of 517 tokens, 32 rows: 32.6 us cut, 20.5 whole) to 15 % more, of 9 and above from 12 % less to 131 % more.
 constexpr int kUnevenShort = 8;
 
 template <typename T>
