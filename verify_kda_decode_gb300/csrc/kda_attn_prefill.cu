@@ -35,7 +35,7 @@
 //
 // 4-bit caches: a code times its block's E4M3 scale is exact in a half (two significant bits by four, 2^-10 to 2688), so the tiles are
 // halves, converted from 72 bytes a key of 128 dims.  Warp 14 brings whole pages' bytes by bulk copies and warps 8-11 only convert;
-// bfloat16 queries come by TMA and are brought to halves in place by the softmax's threads.  4 x 4096 tokens, 32/8 heads: 510 us
+// bfloat16 queries come by TMA and are brought to halves in place by the softmax's threads.  4 x 4096 tokens, 32/8 heads: 516 us
 // (16-bit caches 395).  As with E4M3 codes, the four warps looking up, fetching and converting, 824 us: a fetch took 1350 clocks
 // beside a conversion of 650; with addresses once a tile 738; bulk copies 536.  Without the conversion's instructions 450: they
 // share the issue slots and shared memory with the softmax, and neither waits long for the other.
